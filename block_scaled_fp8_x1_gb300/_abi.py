@@ -53,6 +53,23 @@ class GemmOpts(ctypes.Structure):
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
+F32 = ctypes.c_float
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = [("h", P), ("ldh", I64), ("y", P), ("ldy", I64), ("post_gamma", P), ("gate", P),
+                ("pre_gamma", P), ("alpha", F32), ("eps", F32), ("h_out", P), ("z", P), ("q", P),
+                ("s", P), ("qT", P), ("sT", P), ("qh", P), ("sh", P), ("qy", P), ("sy", P),
+                ("r_pre", P), ("r_post", P)]
+
+
+class ResidualNormBwdArgs(ctypes.Structure):
+    _fields_ = [("dz", P), ("lddz", I64), ("dh", P), ("lddh", I64), ("h", P), ("ldh", I64),
+                ("qh", P), ("sh", P), ("y", P), ("ldy", I64), ("qy", P), ("sy", P),
+                ("post_gamma", P), ("gate", P), ("pre_gamma", P), ("alpha", F32), ("r_pre", P),
+                ("r_post", P), ("dh_out", P), ("dy", P), ("dpre", P), ("dpost", P), ("dgate", P)]
+
+
 ST = ctypes.c_int
 STREAM = ctypes.c_void_p
 
@@ -72,6 +89,10 @@ SIGNATURES = {
     "fp8rl_silu_mul_bwd_quant": (ST, [P, P, I64, I64, P, P, P, P, STREAM]),
     "fp8rl_rmsnorm_bwd": (ST, [P, P, P, P, I64, I64, P, P, P, ctypes.c_size_t, STREAM]),
     "fp8rl_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+    "fp8rl_residual_norm": (ST, [ctypes.POINTER(ResidualNormArgs), I64, I64, STREAM]),
+    "fp8rl_residual_norm_bwd": (ST, [ctypes.POINTER(ResidualNormBwdArgs), I64, I64, P,
+                                     ctypes.c_size_t, STREAM]),
+    "fp8rl_residual_norm_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
     "fp8rl_gemm_fwd": (ST, [P, P, P, P, P, I64, I64, I64, P, ctypes.c_size_t, STREAM]),
     "fp8rl_gemm_dgrad": (ST, [P, P, P, P, P, I64, I64, I64, P, ctypes.c_size_t, STREAM]),
     "fp8rl_gemm_wgrad": (ST, [P, P, P, P, P, I64, I64, I64, P, ctypes.c_size_t, STREAM]),

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/fp8rl.h"
+#include "block.h"
 #include "gemm.h"
 #include "rollout.h"
 
@@ -699,6 +700,95 @@ fp8rl_status fp8rl_rmsnorm_bwd(const uint16_t* x, const uint16_t* gamma, const f
     }
     return cuda_status(launch_rmsnorm_bwd(x, gamma, rstd, dy, M, K, dx, dgamma, reinterpret_cast<float*>(ws),
                                           nblocks, stream));
+}
+
+// ---------------------------------------------------------------- residual + norms
+
+// A tensor of rows given by pointer and row stride: 16-byte aligned, stride >= K and a
+// multiple of 8 elements.
+static fp8rl_status check_rows(const uint16_t* x, int64_t ld, int64_t K) {
+    if (!x || ld < K) return FP8RL_ERR_INVALID_ARG;
+    return aligned16(x) && ld % 8 == 0 ? FP8RL_OK : FP8RL_ERR_ALIGN;
+}
+// A quantized tensor given by its codes and scales, both or neither.
+static fp8rl_status check_pair(const void* q, const void* s) {
+    if ((q == nullptr) != (s == nullptr)) return FP8RL_ERR_INVALID_ARG;
+    return aligned16(q) && aligned16(s) ? FP8RL_OK : FP8RL_ERR_ALIGN;   // null is aligned
+}
+
+fp8rl_status fp8rl_residual_norm(const fp8rl_residual_norm_args* args, int64_t M, int64_t K, fp8rl_stream_t stream) {
+    if (!args || M < 0 || K <= 0) return FP8RL_ERR_INVALID_ARG;
+    const fp8rl_residual_norm_args& a = *args;
+    if (!(a.eps >= 0.0f) || a.eps > 3.0e38f || !(a.alpha >= -3.0e38f && a.alpha <= 3.0e38f)) return FP8RL_ERR_INVALID_ARG;
+    if (K % 128 != 0 || K > kResNormMaxK) return FP8RL_ERR_SHAPE;
+    if (a.qT && M % 128 != 0) return FP8RL_ERR_SHAPE;
+    if (M == 0) return FP8RL_OK;
+    fp8rl_status e = check_rows(a.h, a.ldh, K);
+    if (e == FP8RL_OK) e = check_rows(a.y, a.ldy, K);
+    if (e == FP8RL_OK) e = check_pair(a.q, a.s);
+    if (e == FP8RL_OK) e = check_pair(a.qT, a.sT);
+    if (e == FP8RL_OK) e = check_pair(a.qh, a.sh);
+    if (e == FP8RL_OK) e = check_pair(a.qy, a.sy);
+    if (e != FP8RL_OK) return e;
+    if (!a.pre_gamma || !a.h_out || !a.r_pre || (a.post_gamma && !a.r_post)) return FP8RL_ERR_INVALID_ARG;
+    if (!a.z && !a.q && !a.qT) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(a.pre_gamma) || !aligned16(a.post_gamma) || !aligned16(a.gate) || !aligned16(a.h_out) ||
+        !aligned16(a.z) || !aligned16(a.r_pre) || !aligned16(a.r_post))
+        return FP8RL_ERR_ALIGN;
+    // in place only row for row: h_out is [M][K]
+    if (a.h_out == a.h && a.ldh != K) return FP8RL_ERR_INVALID_ARG;
+    int sms = 0;
+    e = current_device(&sms);
+    if (e != FP8RL_OK) return e;
+    e = cuda_status(launch_residual_norm(a, M, K, sms, stream));
+    if (e != FP8RL_OK || !a.qT) return e;
+    return cuda_status(launch_rmsnorm_cols(a.h_out, a.pre_gamma, a.r_pre, M, K, a.qT, a.sT, g_timeout_ns.load(), stream));
+}
+
+size_t fp8rl_residual_norm_bwd_workspace_bytes(int64_t M, int64_t K) {
+    if (M <= 0 || K <= 0 || K % 128 != 0 || K > kResNormMaxK) return 0;
+    int sms = 0;
+    if (current_device(&sms) != FP8RL_OK) sms = 152;
+    return (size_t)residual_norm_bwd_blocks(M, K, sms) * 3 * (size_t)K * sizeof(float);
+}
+
+fp8rl_status fp8rl_residual_norm_bwd(const fp8rl_residual_norm_bwd_args* args, int64_t M, int64_t K, void* ws,
+                                     size_t ws_bytes, fp8rl_stream_t stream) {
+    if (!args || M < 0 || K <= 0) return FP8RL_ERR_INVALID_ARG;
+    const fp8rl_residual_norm_bwd_args& a = *args;
+    if (!(a.alpha >= -3.0e38f && a.alpha <= 3.0e38f)) return FP8RL_ERR_INVALID_ARG;
+    if (K % 128 != 0 || K > kResNormMaxK) return FP8RL_ERR_SHAPE;
+    if (!a.dpre || (a.post_gamma && !a.dpost) || (a.gate && !a.dgate)) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(a.dpre) || !aligned16(a.dpost) || !aligned16(a.dgate)) return FP8RL_ERR_ALIGN;
+    if (M == 0) {
+        cudaError_t c = cudaMemsetAsync(a.dpre, 0, (size_t)K * sizeof(float), stream);
+        if (c == cudaSuccess && a.post_gamma) c = cudaMemsetAsync(a.dpost, 0, (size_t)K * sizeof(float), stream);
+        if (c == cudaSuccess && a.gate) c = cudaMemsetAsync(a.dgate, 0, (size_t)K * sizeof(float), stream);
+        return cuda_status(c);
+    }
+    const bool need_y = a.post_gamma || a.gate;
+    fp8rl_status e = check_rows(a.dz, a.lddz, K);
+    if (e == FP8RL_OK && a.dh) e = check_rows(a.dh, a.lddh, K);
+    // the saved tensors: both BF16 or both checkpoints
+    if (e == FP8RL_OK) e = check_pair(a.qh, a.sh);
+    if (e == FP8RL_OK && !a.qh) e = check_rows(a.h, a.ldh, K);
+    if (e == FP8RL_OK && need_y) {
+        e = check_pair(a.qy, a.sy);
+        if (e == FP8RL_OK && (a.qy == nullptr) != (a.qh == nullptr)) e = FP8RL_ERR_INVALID_ARG;
+        if (e == FP8RL_OK && !a.qy) e = check_rows(a.y, a.ldy, K);
+    }
+    if (e != FP8RL_OK) return e;
+    if (!a.pre_gamma || !a.r_pre || (a.post_gamma && !a.r_post) || !a.dh_out || !a.dy) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(a.pre_gamma) || !aligned16(a.post_gamma) || !aligned16(a.gate) || !aligned16(a.r_pre) ||
+        !aligned16(a.r_post) || !aligned16(a.dh_out) || !aligned16(a.dy))
+        return FP8RL_ERR_ALIGN;
+    int sms = 0;
+    e = current_device(&sms);
+    if (e != FP8RL_OK) return e;
+    const int nblocks = residual_norm_bwd_blocks(M, K, sms);
+    if (!ws || ws_bytes < (size_t)nblocks * 3 * (size_t)K * sizeof(float)) return FP8RL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return FP8RL_ERR_ALIGN;
+    return cuda_status(launch_residual_norm_bwd(a, M, K, reinterpret_cast<float*>(ws), nblocks, stream));
 }
 
 // ---------------------------------------------------------------- GEMMs

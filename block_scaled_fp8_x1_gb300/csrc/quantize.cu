@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "block.h"
 #include "gemm.h"
 #include "quant_common.cuh"
 
@@ -1132,6 +1133,17 @@ cudaError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* gamma, float
     a.tiles_per_cta = (int)((K / 128) / c);
     if (qT) return launch_panel_t<PRO_RMSNORM, true, true>(a, K, c, st);
     return launch_panel_t<PRO_RMSNORM, true, false>(a, K, c, st);
+}
+
+// the 128x1 codes of the normalised tensor, from the rows' rstd (residual_norm.cu has already
+// written its BF16 or 1x128 form)
+cudaError_t launch_rmsnorm_cols(const uint16_t* x, const uint16_t* gamma, const float* rstd, int64_t M, int64_t K,
+                                uint8_t* qT, float* sT, uint64_t timeout_ns, cudaStream_t st) {
+    PanelArgs a = {};
+    a.x = x; a.ldx = K; a.gamma = gamma; a.rstd_out = const_cast<float*>(rstd);
+    a.M = M; a.K = K; a.qT = qT; a.sT = sT;
+    a.timeout_ns = timeout_ns;
+    return launch_panel_t<PRO_RMSNORM_G, false, true>(a, K, 0, st);
 }
 
 cudaError_t launch_quant_128x128(const uint16_t* w, int64_t N, int64_t K, int64_t ldw, uint8_t* q,

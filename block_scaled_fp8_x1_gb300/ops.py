@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -261,6 +261,165 @@ def rmsnorm_bwd(x: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor, dy: to
                                   _ptr(dgamma), _ptr(ws), ws.numel() if ws is not None else 0,
                                   _stream(dev)), "fp8rl_rmsnorm_bwd")
     return dx, dgamma
+
+
+# ------------------------------------------------------------------ residual + norms
+
+Checkpoint = Tuple[torch.Tensor, torch.Tensor]    # codes u8 [M,K], scales f32 [K/128,M]
+
+
+class ResidualNorm(NamedTuple):
+    """What residual_norm returns; None where it was not asked for."""
+    h: torch.Tensor                        # h' bf16 [M,K]
+    z: Optional[torch.Tensor]              # bf16 [M,K]
+    q: Optional[torch.Tensor]              # z in 1x128: u8 [M,K], f32 [K/128,M]
+    s: Optional[torch.Tensor]
+    qT: Optional[torch.Tensor]             # z in 128x1: u8 [K,M], f32 [M/128,K]
+    sT: Optional[torch.Tensor]
+    r_pre: torch.Tensor                    # f32 [M]
+    r_post: Optional[torch.Tensor]         # f32 [M], with a post norm
+    h_ckpt: Optional[Checkpoint]           # 8-bit checkpoints of h' and y
+    y_ckpt: Optional[Checkpoint]
+
+
+class ResidualNormGrads(NamedTuple):
+    """What residual_norm_bwd returns; None for a parameter that the forward did not have."""
+    dh: torch.Tensor                       # gradient of h, bf16 [M,K]
+    dy: torch.Tensor                       # bf16 [M,K]
+    dpre: torch.Tensor                     # f32 [K]
+    dpost: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+
+
+def _rows(t: torch.Tensor, name: str, shape, device) -> int:
+    """Checks a bf16 matrix of contiguous rows and returns its row stride."""
+    _require(t, torch.bfloat16, name, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t: Optional[torch.Tensor], name: str, dtype, n: int, device) -> None:
+    if t is None:
+        return
+    _require(t, dtype, name, device)
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(t.shape)}")
+    _contig(t, name)
+
+
+def _codes(M: int, K: int, dev) -> Checkpoint:
+    return (torch.empty((M, K), dtype=torch.uint8, device=dev),
+            torch.empty((K // 128, M), dtype=torch.float32, device=dev))
+
+
+def _matrix(t: torch.Tensor, name: str) -> None:
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+
+
+def residual_norm(h: torch.Tensor, y: torch.Tensor, pre_gamma: torch.Tensor, eps: float, *,
+                  post_gamma: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  alpha: float = 1.0, emit: str = "fp8", checkpoint: bool = False,
+                  inplace: bool = False) -> ResidualNorm:
+    """h' = h + alpha gate norm(y) post_gamma and z = norm(h') pre_gamma in one pass.
+
+    h, y bf16 [M,K] (rows may be strided); pre_gamma, post_gamma, gate bf16 [K].  Without
+    post_gamma the block's output y is added as it is; without gate the gate is 1.  `emit`:
+    "bf16" (z), "fp8" (q, s: z quantized 1x128) or "dual" (also 128x1, M % 128 == 0).
+    `checkpoint` also returns h' and y in 8 bits for residual_norm_bwd.  `inplace` writes h'
+    over a contiguous h."""
+    _matrix(h, "h")
+    _require(h, torch.bfloat16, "h")
+    M, K = h.shape
+    dev = h.device
+    ldh, ldy = _rows(h, "h", (M, K), dev), _rows(y, "y", (M, K), dev)
+    for t, n in ((pre_gamma, "pre_gamma"), (post_gamma, "post_gamma"), (gate, "gate")):
+        _vector(t, n, torch.bfloat16, K, dev)
+    if emit not in ("bf16", "fp8", "dual"):
+        raise ValueError(f"emit: expected 'bf16', 'fp8' or 'dual', got {emit!r}")
+    if inplace and not h.is_contiguous():
+        raise ValueError("h: expected a contiguous tensor to write over")
+    h_out = h if inplace else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    z = q = s = qT = sT = h_ckpt = y_ckpt = r_post = None
+    if emit == "bf16":
+        z = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    else:
+        q, s = _codes(M, K, dev)
+    if emit == "dual":
+        qT, sT = _codes(K, M, dev)
+    if checkpoint:
+        h_ckpt, y_ckpt = _codes(M, K, dev), _codes(M, K, dev)
+    r_pre = torch.empty(M, dtype=torch.float32, device=dev)
+    if post_gamma is not None:
+        r_post = torch.empty(M, dtype=torch.float32, device=dev)
+    qh, sh = h_ckpt or (None, None)
+    qy, sy = y_ckpt or (None, None)
+    args = _abi.ResidualNormArgs(
+        _ptr(h), ldh, _ptr(y), ldy, _ptr(post_gamma), _ptr(gate), _ptr(pre_gamma), float(alpha), float(eps),
+        _ptr(h_out), _ptr(z), _ptr(q), _ptr(s), _ptr(qT), _ptr(sT), _ptr(qh), _ptr(sh), _ptr(qy), _ptr(sy),
+        _ptr(r_pre), _ptr(r_post))
+    check(lib().fp8rl_residual_norm(ctypes.byref(args), M, K, _stream(dev)), "fp8rl_residual_norm")
+    return ResidualNorm(h_out, z, q, s, qT, sT, r_pre, r_post, h_ckpt, y_ckpt)
+
+
+def _saved(t, name: str, shape, dev):
+    """(bf16 pointer, row stride, codes, scales) of a saved tensor: bf16 or a checkpoint."""
+    if isinstance(t, torch.Tensor):
+        ld = _rows(t, name, shape, dev)
+        return _ptr(t), ld, None, None
+    q, s = t
+    M, K = shape
+    for c, n, dt, sh in ((q, f"{name} codes", torch.uint8, (M, K)), (s, f"{name} scales", torch.float32, (K // 128, M))):
+        _require(c, dt, n, dev)
+        if tuple(c.shape) != sh:
+            raise ValueError(f"{n}: expected shape {sh}, got {tuple(c.shape)}")
+        _contig(c, n)
+    return None, 0, _ptr(q), _ptr(s)
+
+
+def residual_norm_bwd(dz: torch.Tensor, dh: Optional[torch.Tensor], h: Union[torch.Tensor, Checkpoint],
+                      y: Union[torch.Tensor, Checkpoint, None], pre_gamma: torch.Tensor, r_pre: torch.Tensor, *,
+                      post_gamma: Optional[torch.Tensor] = None, r_post: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, alpha: float = 1.0) -> ResidualNormGrads:
+    """Gradients of residual_norm from dz (of z) and dh (of h', None for zero), both bf16.
+
+    h is the forward's h', y its block output: bf16, or both the forward's 8-bit checkpoints.
+    y is needed only with post_gamma or gate.  r_pre, r_post are the forward's."""
+    _matrix(dz, "dz")
+    _require(dz, torch.bfloat16, "dz")
+    M, K = dz.shape
+    dev = dz.device
+    lddz = _rows(dz, "dz", (M, K), dev)
+    lddh = _rows(dh, "dh", (M, K), dev) if dh is not None else 0
+    for t, n in ((pre_gamma, "pre_gamma"), (post_gamma, "post_gamma"), (gate, "gate")):
+        _vector(t, n, torch.bfloat16, K, dev)
+    _vector(r_pre, "r_pre", torch.float32, M, dev)
+    _vector(r_post, "r_post", torch.float32, M, dev)
+    if post_gamma is not None and r_post is None:
+        raise ValueError("r_post: needed with post_gamma")
+    ph, ldh, qh, sh = _saved(h, "h", (M, K), dev)
+    py, ldy, qy, sy = None, 0, None, None
+    if post_gamma is not None or gate is not None:
+        if y is None:
+            raise ValueError("y: needed with post_gamma or gate")
+        if isinstance(y, torch.Tensor) != isinstance(h, torch.Tensor):
+            raise ValueError("h, y: expected both bf16 or both checkpoints")
+        py, ldy, qy, sy = _saved(y, "y", (M, K), dev)
+    vec = [torch.empty(K, dtype=torch.float32, device=dev) if p is not None else None
+           for p in (pre_gamma, post_gamma, gate)]
+    dh_out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    dy = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    # a buffer of this call's own (not the shared one): calls may run on several streams
+    ws = torch.empty(int(lib().fp8rl_residual_norm_bwd_workspace_bytes(M, K)), dtype=torch.uint8, device=dev)
+    args = _abi.ResidualNormBwdArgs(
+        _ptr(dz), lddz, _ptr(dh), lddh, ph, ldh, qh, sh, py, ldy, qy, sy, _ptr(post_gamma), _ptr(gate),
+        _ptr(pre_gamma), float(alpha), _ptr(r_pre), _ptr(r_post), _ptr(dh_out), _ptr(dy), *map(_ptr, vec))
+    check(lib().fp8rl_residual_norm_bwd(ctypes.byref(args), M, K, _ptr(ws), ws.numel(), _stream(dev)),
+          "fp8rl_residual_norm_bwd")
+    return ResidualNormGrads(dh_out, dy, *vec)
 
 
 # ------------------------------------------------------------------ GEMMs

@@ -194,6 +194,74 @@ FP8RL_API fp8rl_status fp8rl_rmsnorm_bwd(const uint16_t* x, const uint16_t* gamm
 FP8RL_API size_t fp8rl_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
 
 /* ----------------------------------------------------------------------------------------
+ * The norms before and after a block, fused with the block's gate, its residual scale, the
+ * residual add and the quantizer of the next linear.  "Quantization Scheme": the activation
+ * saved for the backward pass is FP8, produced by the preceding fused operator.
+ *   n  = y r(y) g_post  (n = y when post_gamma is NULL),  r(v) = 1/sqrt(mean(v^2) + eps)
+ *   h' = bf16_rne(h + alpha gate n)  (gate = 1 when NULL)
+ *   z  = bf16_rne((h' r(h')) g_pre)
+ * evaluated in FP32.  With post_gamma = gate = NULL and alpha = 1 this is the residual add
+ * and norm of a pre-norm block.  A row's result depends on that row alone: a token gives
+ * the same bits in a batch of one and in a training batch.
+ * -------------------------------------------------------------------------------------- */
+typedef struct {
+    const uint16_t* h; int64_t ldh;    /* residual stream BF16 [M][ldh] */
+    const uint16_t* y; int64_t ldy;    /* the block's output BF16 [M][ldy] */
+    const uint16_t* post_gamma;        /* BF16 [K], nullable: no post norm */
+    const uint16_t* gate;              /* BF16 [K], nullable */
+    const uint16_t* pre_gamma;         /* BF16 [K] */
+    float alpha, eps;                  /* residual scale; eps of both norms */
+    uint16_t* h_out;                   /* h' BF16 [M][K]; may be h itself when ldh == K */
+    uint16_t* z;                       /* BF16 [M][K], nullable */
+    uint8_t* q; float* s;              /* z in 1x128: [M][K], [K/128][M]; both or neither */
+    uint8_t* qT; float* sT;            /* z in 128x1, transposed: [K][M], [M/128][K]; both or
+                                        * neither; needs M % 128 == 0 */
+    uint8_t* qh; float* sh;            /* 8-bit checkpoint of h' (1x128); both or neither */
+    uint8_t* qy; float* sy;            /* 8-bit checkpoint of y (1x128); both or neither */
+    float* r_pre;                      /* r(h') [M] */
+    float* r_post;                     /* r(y) [M]; needed with post_gamma */
+} fp8rl_residual_norm_args;
+
+/* At least one of z, q, qT is set.  K % 128 == 0 and K <= 8192, else FP8RL_ERR_SHAPE.  Other
+ * than h_out on h, outputs overlap nothing. */
+FP8RL_API fp8rl_status fp8rl_residual_norm(const fp8rl_residual_norm_args* args, int64_t M, int64_t K,
+                                           fp8rl_stream_t stream);
+
+/* Its gradients, from the gradients dz of z and dh of h' (dh NULL: zero) and the saved h', y,
+ * r_pre, r_post.  h' and y are BF16, or both 8-bit checkpoints (qh/sh and qy/sy set: the
+ * values decode(code) * scale, in FP32); y is read only with post_gamma or gate.
+ *   x^ = h' r_pre,  t = dz g_pre,  dH = dh + r_pre (t - x^ mean(t x^))
+ *   dn = alpha gate dH,  y^ = y r_post,  u = dn g_post,  dy = r_post (u - y^ mean(u y^))
+ *   (dy = dn without a post norm)
+ *   dpre = sum_m dz x^,  dpost = sum_m dn y^,  dgate = sum_m alpha dH n
+ * dh_out = bf16(dH) is the gradient of h.  dpost is written with post_gamma, dgate with gate.
+ * The sums run in a fixed order: repeated calls give the same bits.  Every output overlaps
+ * nothing.  ws: fp8rl_residual_norm_bwd_workspace_bytes(M, K), no initial contents. */
+typedef struct {
+    const uint16_t* dz; int64_t lddz;  /* BF16 [M][lddz] */
+    const uint16_t* dh; int64_t lddh;  /* BF16 [M][lddh], nullable */
+    const uint16_t* h; int64_t ldh;    /* h' BF16 [M][ldh], when qh is NULL */
+    const uint8_t* qh; const float* sh;
+    const uint16_t* y; int64_t ldy;    /* BF16 [M][ldy], when qy is NULL */
+    const uint8_t* qy; const float* sy;
+    const uint16_t* post_gamma;        /* BF16 [K], nullable */
+    const uint16_t* gate;              /* BF16 [K], nullable */
+    const uint16_t* pre_gamma;         /* BF16 [K] */
+    float alpha;
+    const float* r_pre;                /* [M] */
+    const float* r_post;               /* [M], with post_gamma */
+    uint16_t* dh_out;                  /* BF16 [M][K] */
+    uint16_t* dy;                      /* BF16 [M][K] */
+    float* dpre;                       /* [K] */
+    float* dpost;                      /* [K], with post_gamma */
+    float* dgate;                      /* [K], with gate */
+} fp8rl_residual_norm_bwd_args;
+
+FP8RL_API fp8rl_status fp8rl_residual_norm_bwd(const fp8rl_residual_norm_bwd_args* args, int64_t M, int64_t K,
+                                               void* ws, size_t ws_bytes, fp8rl_stream_t stream);
+FP8RL_API size_t fp8rl_residual_norm_bwd_workspace_bytes(int64_t M, int64_t K);
+
+/* ----------------------------------------------------------------------------------------
  * Block-scaled FP8 GEMMs ("Quantization Scheme": forward, DGrad and WGrad in FP8).
  * Output element = bf16_rne( sum_kb sA(kb,row) * sB(kb,col) * sum_{k in kb} a*b ), with
  * the inner block sum in FP32 on the tensor cores and the outer sum in FP32 registers.

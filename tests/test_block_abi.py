@@ -1,0 +1,76 @@
+"""Host-side argument checks of the block operators: every refusal answers without a GPU and
+launches nothing (the pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+
+FAKE, ODD = 0x10000, 0x10004
+
+
+@pytest.fixture(scope="module")
+def abi():
+    from block_scaled_fp8_x1_gb300 import build_library
+    from block_scaled_fp8_x1_gb300 import _abi
+    build_library()
+    return _abi
+
+
+def norm_args(abi, **kw):
+    base = dict(h=FAKE, ldh=256, y=FAKE, ldy=256, pre_gamma=FAKE, alpha=1.0, eps=1e-5, h_out=FAKE + 4096, z=FAKE,
+                r_pre=FAKE)
+    return abi.ResidualNormArgs(**{**base, **kw})
+
+
+@pytest.mark.parametrize("kw,M,K,status", [
+    ({}, -1, 256, "INVALID_ARG"), ({}, 4, 0, "INVALID_ARG"), ({}, 4, 200, "SHAPE"), ({}, 4, 8320, "SHAPE"),
+    (dict(eps=-1.0), 4, 256, "INVALID_ARG"), (dict(eps=float("nan")), 4, 256, "INVALID_ARG"),
+    (dict(alpha=float("inf")), 4, 256, "INVALID_ARG"), (dict(alpha=float("nan")), 4, 256, "INVALID_ARG"),
+    (dict(h=None), 4, 256, "INVALID_ARG"), (dict(y=None), 4, 256, "INVALID_ARG"),
+    (dict(pre_gamma=None), 4, 256, "INVALID_ARG"), (dict(h_out=None), 4, 256, "INVALID_ARG"),
+    (dict(r_pre=None), 4, 256, "INVALID_ARG"), (dict(post_gamma=FAKE), 4, 256, "INVALID_ARG"),
+    (dict(z=None), 4, 256, "INVALID_ARG"), (dict(q=FAKE), 4, 256, "INVALID_ARG"),
+    (dict(sT=FAKE), 128, 256, "INVALID_ARG"), (dict(qh=FAKE), 4, 256, "INVALID_ARG"),
+    (dict(sy=FAKE), 4, 256, "INVALID_ARG"), (dict(qT=FAKE, sT=FAKE), 100, 256, "SHAPE"),
+    (dict(ldh=128), 4, 256, "INVALID_ARG"), (dict(ldy=128), 4, 256, "INVALID_ARG"),
+    (dict(ldy=260), 4, 256, "ALIGN"), (dict(h=ODD), 4, 256, "ALIGN"), (dict(z=ODD), 4, 256, "ALIGN"),
+    (dict(gate=ODD), 4, 256, "ALIGN"), (dict(q=FAKE, s=ODD), 4, 256, "ALIGN"), (dict(r_pre=ODD), 4, 256, "ALIGN"),
+    (dict(h_out=FAKE, ldh=264), 4, 256, "INVALID_ARG"),
+    (dict(h=None, y=None, z=None), 0, 256, "OK"),
+])
+def test_residual_norm_refusals(abi, kw, M, K, status):
+    want = getattr(abi, "FP8RL_OK" if status == "OK" else f"FP8RL_ERR_{status}")
+    assert abi.lib().fp8rl_residual_norm(ctypes.byref(norm_args(abi, **kw)), M, K, None) == want
+
+
+def bwd_args(abi, **kw):
+    base = dict(dz=FAKE, lddz=256, dh=FAKE, lddh=256, h=FAKE, ldh=256, y=FAKE, ldy=256, pre_gamma=FAKE, alpha=1.0,
+                r_pre=FAKE, dh_out=FAKE, dy=FAKE, dpre=FAKE)
+    return abi.ResidualNormBwdArgs(**{**base, **kw})
+
+
+GATED = dict(gate=FAKE, dgate=FAKE)
+
+
+@pytest.mark.parametrize("kw,M,K,status", [
+    ({}, -1, 256, "INVALID_ARG"), ({}, 4, 200, "SHAPE"), ({}, 4, 8320, "SHAPE"),
+    (dict(alpha=float("nan")), 4, 256, "INVALID_ARG"), (dict(dz=None), 4, 256, "INVALID_ARG"),
+    (dict(h=None), 4, 256, "INVALID_ARG"), (dict(r_pre=None), 4, 256, "INVALID_ARG"),
+    (dict(dpre=None), 4, 256, "INVALID_ARG"), (dict(dy=None), 4, 256, "INVALID_ARG"),
+    (dict(gate=FAKE), 4, 256, "INVALID_ARG"), (dict(post_gamma=FAKE, r_post=FAKE), 4, 256, "INVALID_ARG"),
+    (dict(post_gamma=FAKE, dpost=FAKE), 4, 256, "INVALID_ARG"), (dict(qh=FAKE), 4, 256, "INVALID_ARG"),
+    (dict(y=None, **GATED), 4, 256, "INVALID_ARG"), (dict(qh=FAKE, sh=FAKE, **GATED), 4, 256, "INVALID_ARG"),
+    (dict(qy=FAKE, sy=FAKE, **GATED), 4, 256, "INVALID_ARG"), (dict(lddz=128), 4, 256, "INVALID_ARG"),
+    (dict(lddh=252), 4, 256, "INVALID_ARG"), (dict(ldh=260), 4, 256, "ALIGN"), (dict(dz=ODD), 4, 256, "ALIGN"),
+    (dict(dpre=ODD), 4, 256, "ALIGN"), (dict(qh=FAKE, sh=ODD), 4, 256, "ALIGN"),
+])
+def test_residual_norm_bwd_refusals(abi, kw, M, K, status):
+    want = getattr(abi, f"FP8RL_ERR_{status}")
+    L = abi.lib()
+    assert L.fp8rl_residual_norm_bwd(ctypes.byref(bwd_args(abi, **kw)), M, K, FAKE, 1 << 30, None) == want
+
+
+def test_residual_norm_bwd_workspace(abi):
+    f = abi.lib().fp8rl_residual_norm_bwd_workspace_bytes
+    assert f(0, 256) == 0 and f(4, 200) == 0 and f(4, 8320) == 0
+    assert f(1, 256) == 3 * 256 * 4                    # one row, one block
+    assert f(1 << 20, 5120) <= 160 * 3 * 5120 * 4      # one block per SM at this width
