@@ -89,6 +89,8 @@ SIGNATURES = {
     "fp8rl_silu_mul_bwd_quant": (ST, [P, P, I64, I64, P, P, P, P, STREAM]),
     "fp8rl_rmsnorm_bwd": (ST, [P, P, P, P, I64, I64, P, P, P, ctypes.c_size_t, STREAM]),
     "fp8rl_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
+    "fp8rl_silu_mul_quant_ckpt": (ST, [P, I64, I64, P, P, P, P, P, P, STREAM]),
+    "fp8rl_silu_mul_bwd_quant_ckpt": (ST, [P, P, P, I64, I64, P, P, P, P, STREAM]),
     "fp8rl_residual_norm": (ST, [ctypes.POINTER(ResidualNormArgs), I64, I64, STREAM]),
     "fp8rl_residual_norm_bwd": (ST, [ctypes.POINTER(ResidualNormBwdArgs), I64, I64, P,
                                      ctypes.c_size_t, STREAM]),

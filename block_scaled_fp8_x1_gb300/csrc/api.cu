@@ -791,6 +791,39 @@ fp8rl_status fp8rl_residual_norm_bwd(const fp8rl_residual_norm_bwd_args* args, i
     return cuda_status(launch_residual_norm_bwd(a, M, K, reinterpret_cast<float*>(ws), nblocks, stream));
 }
 
+// ---------------------------------------------------------------- 8-bit checkpoint of gate_up
+
+fp8rl_status fp8rl_silu_mul_quant_ckpt(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s, uint8_t* qT,
+                                       float* sT, uint8_t* qgu, float* sgu, fp8rl_stream_t stream) {
+    if (M < 0 || I <= 0) return FP8RL_ERR_INVALID_ARG;
+    if ((qT == nullptr) != (sT == nullptr)) return FP8RL_ERR_INVALID_ARG;
+    if (I % 128 != 0) return FP8RL_ERR_SHAPE;
+    if (qT && M % 128 != 0) return FP8RL_ERR_SHAPE;
+    if (M == 0) return FP8RL_OK;
+    if (!gu || !q || !s || !qgu || !sgu) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(gu) || !aligned16(q) || !aligned16(s) || !aligned16(qgu) || !aligned16(sgu)) return FP8RL_ERR_ALIGN;
+    if (qT && (!aligned16(qT) || !aligned16(sT))) return FP8RL_ERR_ALIGN;
+    fp8rl_status e = current_device(nullptr);
+    if (e != FP8RL_OK) return e;
+    return cuda_status(launch_silu_mul_quant_ckpt(gu, M, I, q, s, qT, sT, qgu, sgu, g_timeout_ns.load(), stream));
+}
+
+fp8rl_status fp8rl_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const float* sgu, const uint16_t* dh, int64_t M,
+                                           int64_t I, uint8_t* q, float* s, uint8_t* qT, float* sT,
+                                           fp8rl_stream_t stream) {
+    if (M < 0 || I <= 0) return FP8RL_ERR_INVALID_ARG;
+    if ((qT == nullptr) != (sT == nullptr)) return FP8RL_ERR_INVALID_ARG;
+    if (I % 128 != 0) return FP8RL_ERR_SHAPE;
+    if (qT && M % 128 != 0) return FP8RL_ERR_SHAPE;
+    if (M == 0) return FP8RL_OK;
+    if (!qgu || !sgu || !dh || !q || !s) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(qgu) || !aligned16(sgu) || !aligned16(dh) || !aligned16(q) || !aligned16(s)) return FP8RL_ERR_ALIGN;
+    if (qT && (!aligned16(qT) || !aligned16(sT))) return FP8RL_ERR_ALIGN;
+    fp8rl_status e = current_device(nullptr);
+    if (e != FP8RL_OK) return e;
+    return cuda_status(launch_silu_mul_bwd_quant_ckpt(qgu, sgu, dh, M, I, q, s, qT, sT, g_timeout_ns.load(), stream));
+}
+
 // ---------------------------------------------------------------- GEMMs
 
 size_t fp8rl_gemm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K) {

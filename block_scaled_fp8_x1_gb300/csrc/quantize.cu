@@ -89,14 +89,18 @@ __global__ void __launch_bounds__(256) k_quant_1x128(const uint16_t* __restrict_
 // gate / up tiles and the gradient of h (a second tensor map).  PRO_DEQUANT rebuilds the
 // BF16 activation from its saved 1x128 codes and row scales (the stage holds a 128x128
 // code tile and the tile's 128 row scales) for the 128x1 WGrad operand.
+// PRO_SILU_CK is PRO_SILU that also quantizes its gate and up tiles 1x128 (the 8-bit
+// checkpoint of the gate_up output); PRO_SILU_BWD_CK is PRO_SILU_BWD from that checkpoint.
 enum Prologue : int { PRO_COPY = 0, PRO_SILU = 1, PRO_RMSNORM = 2, PRO_RMSNORM_G = 3, PRO_SILU_BWD = 5,
-                      PRO_DEQUANT = 6 };
+                      PRO_DEQUANT = 6, PRO_SILU_BWD_CK = 7, PRO_SILU_CK = 8 };
 
 struct PanelArgs {
     const uint16_t* x;      // COPY / RMSNORM: x[M][ldx];  SILU: gu[M][ldx], ldx = 2*K;
                             // SILU_BWD: gu[M][ldx], ldx = K (K = 2I quantized columns)
-    const uint16_t* x2;     // SILU_BWD: dh[M][K/2]
-    const float* xs;        // DEQUANT: the codes' scales xs[K/128][M] (x holds the codes)
+    const uint16_t* x2;     // SILU_BWD(_CK): dh[M][K/2]
+    const float* xs;        // DEQUANT, SILU_BWD_CK: the codes' scales xs[K/128][M] (x: codes)
+    uint8_t* qc;            // SILU_CK: the checkpoint's codes qc[M][2K] and scales sc[2K/128][M]
+    float* sc;
     int64_t ldx;
     const uint16_t* gamma;  // RMSNORM: gamma[K]
     float eps;
@@ -233,6 +237,55 @@ __device__ __forceinline__ void silu_bwd_pair_from_smem(uint8_t* stage, int R0, 
     fence_proxy_async_smem();
 }
 
+// Two E4M3 codes (a in bits 0-7) to FP32, exactly: through FP16, which holds every finite E4M3.
+__device__ __forceinline__ float2 e4m3_pair(uint32_t pair) {
+    float2 d;
+    asm("{\n\t.reg .b32 h;\n\t.reg .f16 a, b;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
+        "mov.b32 {a, b}, h;\n\t"
+        "cvt.f32.f16 %0, a;\n\t"
+        "cvt.f32.f16 %1, b;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "h"((uint16_t)pair));
+    return d;
+}
+
+// SiLU-mul backward as above from an 8-bit checkpoint: the stage holds the gate and up code
+// tiles (128-byte rows) and the dh tile.  g and u are decode(code) * scale in FP32; `scale` is
+// this lane's row scale (lanes 0-7 of a half-warp the gate's, 8-15 the up's).  dg goes to w, du
+// as BF16 over the dh tile.
+__device__ __forceinline__ void silu_bwd_ckpt_from_smem(uint8_t* stage, int R0, int C0, int lane, float scale, uint32_t (&w)[8][4]) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float sg_ = __shfl_sync(0xffffffffu, scale, (lane & 16) | i);
+        const float su_ = __shfl_sync(0xffffffffu, scale, (lane & 16) | 8 | i);
+        const uint2 gc = *reinterpret_cast<const uint2*>(stage + (R0 + i) * 128 + C0);
+        const uint2 uc = *reinterpret_cast<const uint2*>(stage + 128 * 128 + (R0 + i) * 128 + C0);
+        uint4* dp = reinterpret_cast<uint4*>(stage + 2 * 128 * 128 + (R0 + i) * 256 + C0 * 2);
+        const uint4 d = *dp;
+        const uint32_t dv[4] = {d.x, d.y, d.z, d.w};
+        uint32_t du[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 g2 = __fmul2_rn(e4m3_pair((j < 2 ? gc.x : gc.y) >> (16 * (j & 1))), make_float2(sg_, sg_));
+            const float2 u2 = __fmul2_rn(e4m3_pair((j < 2 ? uc.x : uc.y) >> (16 * (j & 1))), make_float2(su_, su_));
+            float og[2], ou[2];
+            #pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float g = e ? g2.y : g2.x, uu = e ? u2.y : u2.x;
+                const float dd = e ? bf16_hi(dv[j]) : bf16_lo(dv[j]);
+                const float sg = __fdividef(1.0f, 1.0f + __expf(-g));
+                og[e] = __fmul_rn(__fmul_rn(__fmul_rn(dd, uu), sg), __fmaf_rn(g, __fsub_rn(1.0f, sg), 1.0f));
+                ou[e] = __fmul_rn(dd, __fmul_rn(g, sg));
+            }
+            w[i][j] = pack_bf16x2(og[0], og[1]);
+            du[j] = pack_bf16x2(ou[0], ou[1]);
+        }
+        *dp = make_uint4(du[0], du[1], du[2], du[3]);
+    }
+    fence_proxy_async_smem();   // the stage is refilled by TMA after these generic writes
+}
+
 // BF16 unpacking that the compiler may not merge with the plain one: the column codes
 // unpack again instead of keeping all 64 unpacked values live from the row codes.
 __device__ __forceinline__ float bf16_lo_v(uint32_t w) {
@@ -251,6 +304,41 @@ __device__ __forceinline__ float bf16_hi_v(uint32_t w) {
 __device__ __noinline__ uint4 encode4_slow(float2 x0, float2 x1, float2 x2, float2 x3, float s) {
     return make_uint4(e4m3x2(__fdiv_rn(x0.x, s), __fdiv_rn(x0.y, s)), e4m3x2(__fdiv_rn(x1.x, s), __fdiv_rn(x1.y, s)),
                       e4m3x2(__fdiv_rn(x2.x, s), __fdiv_rn(x2.y, s)), e4m3x2(__fdiv_rn(x3.x, s), __fdiv_rn(x3.y, s)));
+}
+
+// 1x128 codes and scales of one thread's 8 rows (from row r0) x 8 columns (C0 ..) of column
+// block tt, q[M][ldq]; a row's group is the 16 lanes of the half-warp.
+__device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_t* q, float* s, int64_t ldq, int64_t M,
+                                               int64_t r0, int64_t tt, int C0, int lane) {
+    const int cl = lane & 15;
+    uint32_t mine = 0;   // maximum of row r0 + (cl & 7)
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t v = absmax2(absmax2(absmax2(absmax2(0u, w[i][0]), w[i][1]), w[i][2]), w[i][3]);
+        #pragma unroll
+        for (int off = 8; off >= 1; off >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
+        if ((cl & 7) == i) mine = max(v & 0xFFFFu, v >> 16);
+    }
+    const FastScale fs = fast_scale(bf16_bits_amax_to_f32(mine));
+    if (cl < 8 && r0 + cl < M) s[tt * M + r0 + cl] = fs.s;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int src = (lane & 16) | i;
+        const float si = __shfl_sync(0xffffffffu, fs.s, src);
+        const float nri = __shfl_sync(0xffffffffu, fs.nr, src);
+        const uint32_t keep = si == 0.0f ? 0u : 0xFFFFFFFFu;
+        uint32_t c[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = encode_pair_neg(make_float2(bf16_lo(w[i][j]), bf16_hi(w[i][j])), si, nri);
+        uint32_t lo = flip_codes(c[0], c[1], keep), hi = flip_codes(c[2], c[3], keep);
+        if (si > 0.0f && scale_is_slow(si)) {
+            const uint4 v = encode4_slow(make_float2(bf16_lo(w[i][0]), bf16_hi(w[i][0])), make_float2(bf16_lo(w[i][1]), bf16_hi(w[i][1])),
+                                         make_float2(bf16_lo(w[i][2]), bf16_hi(w[i][2])), make_float2(bf16_lo(w[i][3]), bf16_hi(w[i][3])), si);
+            lo = v.x | (v.y << 16);
+            hi = v.z | (v.w << 16);
+        }
+        if (r0 + i < M) stg_v2(q + (r0 + i) * ldq + tt * 128 + C0, lo, hi);
+    }
 }
 
 // rstd of every row for PRO_RMSNORM_G: one warp per row.  The squares are summed in
@@ -292,14 +380,15 @@ __global__ void __launch_bounds__(256) k_rms_rstd(const uint16_t* __restrict__ x
 // Input stages of the TMA ring (each a 128x128 BF16 tile; SiLU-mul stages gate and up).
 template <int PRO, bool COLQ>
 struct PanelStages {
-    static constexpr int NIN = (PRO == PRO_SILU) ? 2 : (PRO == PRO_SILU_BWD ? 3 : 1);
+    // SILU_BWD_CK: two 16 KB code tiles (gate, up), then the BF16 dh tile: as many bytes as two
+    static constexpr int NIN = (PRO == PRO_SILU || PRO == PRO_SILU_CK || PRO == PRO_SILU_BWD_CK) ? 2 : (PRO == PRO_SILU_BWD ? 3 : 1);
     // DEQUANT: a 128x128 code tile and its 128 row scales
     static constexpr int STAGE_BYTES = PRO == PRO_DEQUANT ? 128 * 128 + 128 * 4 : NIN * 128 * 128 * 2;
     // SiLU-mul stages 64 KB per tile: one stage lets two CTAs share an SM, which hides the
     // copy latency better than three stages in one CTA (0.186 vs 0.242 ms at 8192x14336).
     // The 128x1 codes pass through two 16 KB shared-memory tiles (COLQ), which leaves room
     // for two input stages of 32 KB at two CTAs per SM.
-    static constexpr int STAGES = (PRO == PRO_SILU || PRO == PRO_SILU_BWD) ? 1 : (COLQ && PRO != PRO_DEQUANT ? 2 : 3);
+    static constexpr int STAGES = (NIN > 1) ? 1 : (COLQ && PRO != PRO_DEQUANT ? 2 : 3);
     static constexpr int COLQ_OFF = ((STAGES * STAGE_BYTES + 127) / 128) * 128;
     // (SiLU-mul backward stages its 128x1 codes in the stage's gate tile, dead after its
     // prologue: no separate staging tiles)
@@ -324,6 +413,8 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
     constexpr bool COLQ = COL_OUT;
     using PS = PanelStages<PRO, COLQ>;
     constexpr int STAGES = PS::STAGES;
+    // an item is a source column block, which gives both its dg and its du tile
+    constexpr bool PAIR = PRO == PRO_SILU_BWD || PRO == PRO_SILU_BWD_CK;
     extern __shared__ uint8_t q_smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q_smem_raw) + 127) & ~uintptr_t(127));
     __shared__ __align__(8) uint64_t full_bar[STAGES];
@@ -343,16 +434,14 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
     constexpr bool PERSIST = PRO != PRO_RMSNORM;
     const int64_t rms_panel = blockIdx.y;
     const int64_t rms_m0 = rms_panel * 128;
-    const int64_t all_tiles = ((a.M + 127) / 128) * (PRO == PRO_SILU_BWD ? ntiles / 2 : ntiles);   // items
+    const int64_t all_tiles = ((a.M + 127) / 128) * (PAIR ? ntiles / 2 : ntiles);   // items
     const int64_t t_begin = PERSIST ? 0 : (int64_t)blockIdx.x * a.tiles_per_cta;
     const int64_t t_end = (t_begin + a.tiles_per_cta < ntiles) ? t_begin + a.tiles_per_cta : ntiles;
     const int n = PERSIST ? (int)((all_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) : (int)(t_end - t_begin);
     const int total = (PRO == PRO_RMSNORM) ? 2 * n : n;   // items streamed through the ring
     auto tile_at = [&](int it, int64_t& pnl, int64_t& tt) {
         if (PERSIST) {
-            // SiLU-mul backward: an item is a source column block, which gives both its dg
-            // and its du tile
-            const int64_t per = PRO == PRO_SILU_BWD ? ntiles / 2 : ntiles;
+            const int64_t per = PAIR ? ntiles / 2 : ntiles;
             const int64_t id = blockIdx.x + (int64_t)(it % n) * gridDim.x;
             pnl = id / per;
             tt = id - pnl * per;
@@ -367,7 +456,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmx);
-        if (PRO == PRO_SILU_BWD) tma_prefetch_desc(&tmy);
+        if (PAIR) tma_prefetch_desc(&tmy);
     }
     __syncthreads();
     // part: 0 every tile of the item; SiLU-mul backward also 1 (the barrier's arrival and
@@ -385,6 +474,10 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             // 512 bytes at a 16-byte-aligned offset, since M is a multiple of 128)
             tma_load_2d(smem_u32(dst), &tmx, bar, (int)k0, (int)m0, 0);
             bulk_load_1d(smem_u32(dst + 128 * 128), a.xs + tt * a.M + m0, 128 * 4, bar);
+        } else if (PRO == PRO_SILU_BWD_CK) {
+            tma_load_2d(smem_u32(dst), &tmx, bar, (int)k0, (int)m0, 0);
+            tma_load_2d(smem_u32(dst + 128 * 128), &tmx, bar, (int)(a.K / 2 + k0), (int)m0, 0);
+            tma_load_2d(smem_u32(dst + 2 * 128 * 128), &tmy, bar, (int)k0, (int)m0, 0);
         } else if (PRO == PRO_SILU_BWD) {
             // output column tile k0 is dg (k0 < I) or du (k0 >= I) of source column block j0:
             // the gate tile, the up tile and the tile of dh of that block
@@ -397,7 +490,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             }
         } else {
             tma_load_2d(smem_u32(dst), &tmx, bar, (int)k0, (int)m0, 0);
-            if (PRO == PRO_SILU) tma_load_2d(smem_u32(dst + 128 * 128 * 2), &tmx, bar, (int)(a.K + k0), (int)m0, 0);
+            if (PRO == PRO_SILU || PRO == PRO_SILU_CK) tma_load_2d(smem_u32(dst + 128 * 128 * 2), &tmx, bar, (int)(a.K + k0), (int)m0, 0);
         }
     };
     int issued = 0;
@@ -471,6 +564,15 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
     }
 
     for (; ok && item < total; ++item) {
+        float ck_scale = 0.0f;
+        if (PRO == PRO_SILU_BWD_CK) {
+            // lane cl holds the gate scale of row R0 + cl (cl < 8) or the up scale of row
+            // R0 + cl - 8 of its half; requested before the wait for the item's tiles
+            int64_t pnl, tt;
+            tile_at(item, pnl, tt);
+            const int64_t m = pnl * 128 + R0 + (cl & 7);
+            if (m < a.M) ck_scale = __ldg(a.xs + (tt + (cl < 8 ? 0 : ntiles / 2)) * a.M + m);
+        }
         ok = wait_item(item);
         if (!ok) break;
         int64_t panel, t;
@@ -720,6 +822,23 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
                 __syncthreads();
                 if (tid == 0 && issued < total) issue(issued++, 2);
             }
+        } else if constexpr (PRO == PRO_SILU_BWD_CK) {
+            // as above; du waits over the dh tile, and the 128x1 codes have staging tiles of
+            // their own, so the whole stage is refilled once du has been read back
+            silu_bwd_ckpt_from_smem(stage, R0, C0, lane, ck_scale, w);
+            quantize_tile(w, t, smem_u32(stages + PS::COLQ_OFF), 0);
+            const float rg0[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            rows_from_smem<PRO_COPY>(stage + 2 * 128 * 128, a, 0, R0, C0, nullptr, rg0, w);
+            quantize_tile(w, ntiles / 2 + t, smem_u32(stages + PS::COLQ_OFF) + 128u * 128u, 1);
+        } else if constexpr (PRO == PRO_SILU_CK) {
+            const float rg0[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            #pragma unroll 1
+            for (int half_gu = 0; half_gu < 2; ++half_gu) {
+                rows_from_smem<PRO_COPY>(stage + half_gu * 128 * 256, a, 0, R0, C0, nullptr, rg0, w);
+                quant_rows_8x8(w, a.qc, a.sc, 2 * a.K, a.M, m0 + R0, half_gu * ntiles + t, C0, lane);
+            }
+            rows_from_smem<PRO_SILU>(stage, a, t * 128, R0, C0, nullptr, rg0, w);
+            quantize_tile(w, t, smem_u32(stages + PS::COLQ_OFF) + (uint32_t)(item & 1) * (128u * 128u), 1);
         } else {
             float rg[8];
             #pragma unroll
@@ -1018,9 +1137,10 @@ static cudaError_t tmap_u8(CUtensorMap* m, const void* base, int64_t rows, int64
 template <int PRO, bool ROW_OUT, bool COL_OUT>
 static cudaError_t launch_panel_t(const PanelArgs& a, int64_t in_cols, int cluster, cudaStream_t st) {
     CUtensorMap tm, tm2;
-    cudaError_t e = PRO == PRO_DEQUANT ? tmap_u8(&tm, a.x, a.M, in_cols) : tmap_bf16(&tm, a.x, a.M, in_cols, a.ldx);
+    constexpr bool pair = PRO == PRO_SILU_BWD || PRO == PRO_SILU_BWD_CK;
+    cudaError_t e = PRO == PRO_DEQUANT || PRO == PRO_SILU_BWD_CK ? tmap_u8(&tm, a.x, a.M, in_cols) : tmap_bf16(&tm, a.x, a.M, in_cols, a.ldx);
     if (e != cudaSuccess) return e;
-    if (PRO == PRO_SILU_BWD) {
+    if (pair) {
         e = tmap_bf16(&tm2, a.x2, a.M, a.K / 2, a.K / 2);
         if (e != cudaSuccess) return e;
     } else {
@@ -1044,7 +1164,7 @@ static cudaError_t launch_panel_t(const PanelArgs& a, int64_t in_cols, int clust
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 256, smem);
             return std::max(1, sms * std::max(1, per_sm));
         }();
-        const int64_t all_tiles = ((a.M + 127) / 128) * (PRO == PRO_SILU_BWD ? ntiles / 2 : ntiles);   // items
+        const int64_t all_tiles = ((a.M + 127) / 128) * (pair ? ntiles / 2 : ntiles);   // items
         cfg.gridDim = dim3((unsigned)std::min<int64_t>(all_tiles, resident), 1, 1);
     }
     cfg.blockDim = dim3(256, 1, 1);
@@ -1092,6 +1212,28 @@ cudaError_t launch_silu_mul_bwd_quant(const uint16_t* gu, const uint16_t* dh, in
     a.timeout_ns = timeout_ns;
     if (qT) return launch_panel_t<PRO_SILU_BWD, true, true>(a, 2 * I, 0, st);
     return launch_panel_t<PRO_SILU_BWD, true, false>(a, 2 * I, 0, st);
+}
+
+// SiLU-mul -> quantize, with the 1x128 codes of its input from the same read
+cudaError_t launch_silu_mul_quant_ckpt(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s, uint8_t* qT,
+                                       float* sT, uint8_t* qgu, float* sgu, uint64_t timeout_ns, cudaStream_t st) {
+    PanelArgs a = {};
+    a.x = gu; a.ldx = 2 * I; a.M = M; a.K = I; a.q = q; a.s = s; a.qT = qT; a.sT = sT; a.qc = qgu; a.sc = sgu;
+    a.timeout_ns = timeout_ns;
+    if (qT) return launch_panel_t<PRO_SILU_CK, true, true>(a, 2 * I, 0, st);
+    return launch_panel_t<PRO_SILU_CK, true, false>(a, 2 * I, 0, st);
+}
+
+// SiLU-mul backward -> dual quantization from that checkpoint
+cudaError_t launch_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const float* sgu, const uint16_t* dh, int64_t M, int64_t I,
+                                           uint8_t* q, float* s, uint8_t* qT, float* sT, uint64_t timeout_ns,
+                                           cudaStream_t st) {
+    PanelArgs a = {};
+    a.x = reinterpret_cast<const uint16_t*>(qgu); a.ldx = 2 * I; a.xs = sgu; a.x2 = dh; a.M = M; a.K = 2 * I;
+    a.q = q; a.s = s; a.qT = qT; a.sT = sT;
+    a.timeout_ns = timeout_ns;
+    if (qT) return launch_panel_t<PRO_SILU_BWD_CK, true, true>(a, 2 * I, 0, st);
+    return launch_panel_t<PRO_SILU_BWD_CK, true, false>(a, 2 * I, 0, st);
 }
 
 // 128x1 WGrad operand rebuilt from the saved 1x128 codes and scales of X

@@ -422,6 +422,46 @@ def residual_norm_bwd(dz: torch.Tensor, dh: Optional[torch.Tensor], h: Union[tor
     return ResidualNormGrads(dh_out, dy, *vec)
 
 
+# ------------------------------------------------------------------ 8-bit checkpoint of gate_up
+
+def silu_mul_quant_ckpt(gu: torch.Tensor, dual: bool = True):
+    """silu_mul_quant of gu bf16 [M, 2I] with an 8-bit checkpoint of gu from the same read:
+    (q [M,I], s [I/128,M], qT [I,M] or None, sT [M/128,I] or None, qgu u8 [M,2I],
+    sgu f32 [2I/128,M])."""
+    _matrix(gu, "gu")
+    _require(gu, torch.bfloat16, "gu")
+    _contig(gu, "gu")
+    M, I2 = gu.shape
+    if I2 % 2 != 0:
+        raise ValueError(f"gu: expected an even number of columns, got {I2}")
+    I, dev = I2 // 2, gu.device
+    q, s = _codes(M, I, dev)
+    qgu, sgu = _codes(M, I2, dev)
+    qT, sT = _codes(I, M, dev) if dual else (None, None)
+    check(lib().fp8rl_silu_mul_quant_ckpt(_ptr(gu), M, I, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT), _ptr(qgu),
+                                          _ptr(sgu), _stream(dev)), "fp8rl_silu_mul_quant_ckpt")
+    return q, s, qT, sT, qgu, sgu
+
+
+def silu_mul_bwd_quant_ckpt(qgu: torch.Tensor, sgu: torch.Tensor, dh: torch.Tensor, dual: bool = True):
+    """silu_mul_bwd_quant from the 8-bit checkpoint qgu u8 [M,2I], sgu f32 [2I/128,M] and dh
+    bf16 [M,I]: (q [M,2I], s [2I/128,M], qT [2I,M] or None, sT [M/128,2I] or None)."""
+    _matrix(qgu, "qgu")
+    _require(qgu, torch.uint8, "qgu")
+    M, I2 = qgu.shape
+    dev = qgu.device
+    _saved((qgu, sgu), "gu", (M, I2), dev)
+    _require(dh, torch.bfloat16, "dh", dev)
+    _contig(dh, "dh")
+    if I2 % 2 != 0 or tuple(dh.shape) != (M, I2 // 2):
+        raise ValueError(f"dh: expected {(M, I2 // 2)}, got {tuple(dh.shape)}")
+    q, s = _codes(M, I2, dev)
+    qT, sT = _codes(I2, M, dev) if dual else (None, None)
+    check(lib().fp8rl_silu_mul_bwd_quant_ckpt(_ptr(qgu), _ptr(sgu), _ptr(dh), M, I2 // 2, _ptr(q), _ptr(s),
+                                              _ptr(qT), _ptr(sT), _stream(dev)), "fp8rl_silu_mul_bwd_quant_ckpt")
+    return q, s, qT, sT
+
+
 # ------------------------------------------------------------------ GEMMs
 
 _ws_lock = threading.Lock()

@@ -193,6 +193,22 @@ FP8RL_API fp8rl_status fp8rl_rmsnorm_bwd(const uint16_t* x, const uint16_t* gamm
                                          fp8rl_stream_t stream);
 FP8RL_API size_t fp8rl_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
 
+/* SiLU-mul -> quantize that also saves its input for the backward pass as an 8-bit
+ * checkpoint, from one read of gu ("Quantization Scheme": activations saved for the backward
+ * pass are FP8, produced by the fused operator).  q, s, qT, sT exactly as
+ * fp8rl_silu_mul_quant; qgu (E4M3 [M][2I]), sgu (float [2I/128][M]) exactly as
+ * fp8rl_quantize_1x128 of gu: half the bytes of gu, which need not be kept. */
+FP8RL_API fp8rl_status fp8rl_silu_mul_quant_ckpt(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q,
+                                                 float* s, uint8_t* qT, float* sT, uint8_t* qgu,
+                                                 float* sgu, fp8rl_stream_t stream);
+
+/* fp8rl_silu_mul_bwd_quant from that checkpoint: the gate and up values are
+ * decode(qgu) * sgu in FP32, everything else as there. */
+FP8RL_API fp8rl_status fp8rl_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const float* sgu,
+                                                     const uint16_t* dh, int64_t M, int64_t I,
+                                                     uint8_t* q, float* s, uint8_t* qT, float* sT,
+                                                     fp8rl_stream_t stream);
+
 /* ----------------------------------------------------------------------------------------
  * The norms before and after a block, fused with the block's gate, its residual scale, the
  * residual add and the quantizer of the next linear.  "Quantization Scheme": the activation

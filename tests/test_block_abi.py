@@ -74,3 +74,18 @@ def test_residual_norm_bwd_workspace(abi):
     assert f(0, 256) == 0 and f(4, 200) == 0 and f(4, 8320) == 0
     assert f(1, 256) == 3 * 256 * 4                    # one row, one block
     assert f(1 << 20, 5120) <= 160 * 3 * 5120 * 4      # one block per SM at this width
+
+
+@pytest.mark.parametrize("M,I,ptr,status", [
+    (-1, 256, {}, "INVALID_ARG"), (4, 0, {}, "INVALID_ARG"), (4, 200, {}, "SHAPE"), (100, 256, dict(qT=FAKE, sT=FAKE), "SHAPE"),
+    (4, 256, dict(qT=FAKE), "INVALID_ARG"), (4, 256, dict(src=None), "INVALID_ARG"), (4, 256, dict(ck=None), "INVALID_ARG"),
+    (4, 256, dict(sck=None), "INVALID_ARG"), (4, 256, dict(q=None), "INVALID_ARG"), (4, 256, dict(src=ODD), "ALIGN"),
+    (4, 256, dict(ck=ODD), "ALIGN"), (4, 256, dict(sck=ODD), "ALIGN"), (128, 256, dict(qT=ODD, sT=FAKE), "ALIGN"),
+    (0, 256, dict(src=None, ck=None, sck=None, q=None), "OK"),
+])
+def test_silu_checkpoint_refusals(abi, M, I, ptr, status):
+    p = {**dict(src=FAKE, q=FAKE, s=FAKE, qT=None, sT=None, ck=FAKE, sck=FAKE), **ptr}
+    want = getattr(abi, "FP8RL_OK" if status == "OK" else f"FP8RL_ERR_{status}")
+    L = abi.lib()
+    assert L.fp8rl_silu_mul_quant_ckpt(p["src"], M, I, p["q"], p["s"], p["qT"], p["sT"], p["ck"], p["sck"], None) == want
+    assert L.fp8rl_silu_mul_bwd_quant_ckpt(p["ck"], p["sck"], p["src"], M, I, p["q"], p["s"], p["qT"], p["sT"], None) == want
