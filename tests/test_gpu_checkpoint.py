@@ -3,8 +3,9 @@
 The forward's outputs are those of the separate operators bit for bit.  The backward is checked
 in two ways: where the checkpoint decodes to BF16 numbers it must give the bits of the BF16
 operator; otherwise every decoded element lies within the roundings of the 64-bit gradient: E4M3
-half a step (2^-4 of the value, 2^-10 of the scale among the subnormals), BF16 half a step (2^-8),
-and 2^-16 of the terms for the FP32 evaluation (its exponential and reciprocal included).
+half a step (2^-4 of the value, 2^-10 of the scale among the subnormals), BF16 half a step (2^-8 of
+the value, 2^-134 among the subnormals, where a saturated gate's gradients lie), and 2^-16 of the
+terms for the FP32 evaluation (its exponential and reciprocal included).
 """
 import pytest
 import torch
@@ -76,7 +77,7 @@ def gradient(gu, dh):
 
 def check_codes(q, s, d, mag):
     M, C = q.shape
-    err = mag * 2.0 ** -16
+    err = mag * 2.0 ** -16 + 2.0 ** -134
     group = lambda x: x.view(M, C // 128, 128)  # noqa: E731
     amax = group(d.abs()).amax(2)
     slack = group(err).amax(2) + ref.BF16_HALF * amax
