@@ -1019,6 +1019,71 @@ fp8rl_status fp8rl_gemm_nvfp4(const uint8_t* qx, const uint8_t* sfx, const float
     return run_gemm_nvf4(qx, sfx, gx, qw, sfw, gw, y, M, N, K, ldy, splits, false, stream);
 }
 
+// How a product of M tokens with an [N][K] weight shares K: the cluster size and the warps of a
+// CTA (matvec.cu).
+static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_req, int* splits, int* wk, int* clusters) {
+    int best_s = 0, best_w = 1;
+    double best = 1e30;
+    for (int s = 1; s <= 8; ++s) {
+        if (splits_req > 0 && s != splits_req) continue;
+        if (s > nkb || matvec_smem(M, (int)nkb, s) > kMatvecMaxSmem) continue;
+        for (int w = 1; w <= 8; w *= 2) {
+            const int per_sm = M <= 8 && matvec_smem(M, (int)nkb, s) <= kMatvecMaxSmem / 2 ? 2 : 1;
+            const int64_t groups = (tiles + 8 / w - 1) / (8 / w), at_once = (int64_t)sms * per_sm / s;
+            const int64_t rounds = (groups + at_once - 1) / at_once;
+            const int64_t units = ((nkb + s - 1) / s + w - 1) / w;
+            const double cost = (double)rounds * ((double)units + (s > 1 ? 1.5 : 0.5));
+            if (cost < best - 1e-9) {
+                best = cost;
+                best_s = s;
+                best_w = w;
+            }
+        }
+    }
+    *splits = best_s;
+    *wk = best_w;
+    if (best_s == 0) return;
+    const int per_sm = M <= 8 && matvec_smem(M, (int)nkb, best_s) <= kMatvecMaxSmem / 2 ? 2 : 1;
+    const int64_t groups = (tiles + 8 / best_w - 1) / (8 / best_w);
+    *clusters = (int)std::min<int64_t>(groups, best_s > 1 ? groups : (int64_t)sms * per_sm);
+}
+
+fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
+                                const uint8_t* sfw, const float* gw, int64_t N, uint16_t* y, int64_t ldy, int splits,
+                                fp8rl_stream_t stream) {
+    if (M < 0 || N < 0 || K <= 0 || ldx < K || ldy < N || splits < 0 || splits > 8) return FP8RL_ERR_INVALID_ARG;
+    if (K % 256 != 0 || N % 128 != 0 || M > kMatvecMaxTokens || N / 32 > 0x7FFFFFF0 || K / 128 > 0x7FFFFF) return FP8RL_ERR_SHAPE;
+    if (M == 0 || N == 0) return FP8RL_OK;
+    if (!x || !qw || !sfw || !gw || !y) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(qw) || !aligned16(sfw) || !aligned16(gw) || !aligned16(y) || ldx % 8 != 0 || ldy % 8 != 0)
+        return FP8RL_ERR_ALIGN;
+    int sms = 0;
+    fp8rl_status e = current_device(&sms);
+    if (e != FP8RL_OK) return e;
+    // tokens per launch: fewer where their slice of x would not fit in shared memory
+    int64_t step = M;
+    while (step > 1 && matvec_smem((int)step, (int)(K / 128), splits > 0 ? splits : 8) > kMatvecMaxSmem) step = (step + 1) / 2;
+    for (int64_t m = 0; m < M; m += step) {
+        MatvecParams p = {};
+        p.M = (int)std::min(step, M - m);
+        p.nkb = (int)(K / 128);
+        p.tiles = (int)(N / 32);
+        int clusters = 0;
+        matvec_plan(p.M, p.nkb, p.tiles, sms, splits, &p.splits, &p.wk, &clusters);
+        if (p.splits == 0) return FP8RL_ERR_SHAPE;   // one token's slice of K does not fit
+        p.x = x + m * ldx;
+        p.ldx = ldx;
+        p.qw = qw;
+        p.sfw = sfw;
+        p.gw = gw;
+        p.y = y + m * ldy;
+        p.ldy = ldy;
+        e = cuda_status(launch_matvec_nvfp4(p, clusters, stream));
+        if (e != FP8RL_OK) return e;
+    }
+    return FP8RL_OK;
+}
+
 fp8rl_status fp8rl_linear_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
                                 const uint8_t* sfw, const float* gw, int64_t N, uint8_t* qx, uint8_t* sfx, float* gx,
                                 uint16_t* y, fp8rl_stream_t stream) {

@@ -1,5 +1,6 @@
 // block.h -- launchers of the block operators around the FP8 linears (internal): the fused
-// residual + norms and its backward, and SiLU-mul with an 8-bit checkpoint of its input.
+// residual + norms and its backward, SiLU-mul with an 8-bit checkpoint of its input, and the
+// product of a few tokens with NVFP4 weights.
 #pragma once
 
 #include "gemm.h"
@@ -26,5 +27,26 @@ cudaError_t launch_silu_mul_quant_ckpt(const uint16_t* gu, int64_t M, int64_t I,
 cudaError_t launch_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const float* sgu, const uint16_t* dh, int64_t M, int64_t I,
                                            uint8_t* q, float* s, uint8_t* qT, float* sT, uint64_t timeout_ns,
                                            cudaStream_t st);
+
+// matvec.cu: y = x W^T for M <= 16 BF16 tokens, W in NVFP4 (codes, scale atoms, row scales).
+struct MatvecParams {
+    int M;                   // tokens, 1..16
+    int nkb;                 // K / 128 (even)
+    int tiles;               // N / 32 (a multiple of 4)
+    int splits;              // CTAs of a cluster that share K, 1..8
+    int wk;                  // warps of a CTA that share K: 1, 2, 4 or 8
+    const uint16_t* x;
+    int64_t ldx;
+    const uint8_t* qw;
+    const uint8_t* sfw;
+    const float* gw;
+    uint16_t* y;
+    int64_t ldy;
+};
+constexpr int kMatvecMaxTokens = 16;
+constexpr size_t kMatvecMaxSmem = 224 * 1024;
+size_t matvec_smem(int M, int nkb, int splits);   // dynamic shared memory of a CTA
+// `clusters` of p.splits CTAs, each taking every clusters-th group of 8 / wk tiles of 32 rows.
+cudaError_t launch_matvec_nvfp4(const MatvecParams& p, int clusters, cudaStream_t st);
 
 }  // namespace fp8rl

@@ -1,0 +1,292 @@
+// matvec.cu -- y = x W^T for 1 to 16 tokens: BF16 activations on NVFP4 weights.
+//
+// "QeRL" (chatpaper.ai), abstract: rollout runs with NVFP4-quantized weights.  Here the weights
+// alone are in 4 bits (nvfp4.cu gives the format and its layouts; the same q, sf, g serve its GEMM):
+//     y[m][n] = bf16( g[n] sum_k x[m][k] e2m1(n,k) e4m3(n, k/16) ),
+// with x as it is.
+//
+// Exactness.  e2m1 (2 significant bits) times e4m3 (4) has 6 and lies in 2^-10 .. 2688, so the
+// weight w = e2m1 e4m3 is an FP16 number.  x goes to FP16 after a power-of-two scale for each token
+// and 128 elements of K that takes their largest magnitude to [2^14, 2^15): its 8 significant bits
+// fit, and only what is below 2^-28 of that maximum loses bits (an error below 2^-39 of it).  So
+// the products are those of the given numbers and the FP16 tensor-core MMA sums them in FP32; the
+// scale comes off in FP32, exactly.
+//
+// Work.  A unit is 32 weight rows x 128 of K: 2 KB of codes and 256 B of scales, which one warp
+// loads straight to registers (PF units ahead) and multiplies with mma.m16n8k16: weights are the M
+// side, up to 8 (or two times 8) tokens the N side.  The order of K inside the MMA is free as long
+// as both operands agree: lane (g, t) = (lane / 4, lane % 4) takes the 16 bytes of K = 32t .. 32t+31
+// of its rows, whose two scales sit in one 16-bit piece of the scale atom, and the matching x.  The
+// rows of a unit are 8 o + g + 32 i (i = 0..3) of a 128-row group, so that one 16-byte load of the
+// scale atom serves a lane's four rows.
+//
+// A CTA of 8 warps works on 8 / WK tiles of 32 rows at a time, WK warps splitting K, and a cluster
+// of S CTAs splits K again; the parts are added in a fixed order (warps, then CTAs) through
+// (distributed) shared memory.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "block.h"
+#include "cluster.cuh"
+#include "common.cuh"
+
+namespace fp8rl {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kXBlock = 320;     // bytes of one token's 128 FP16 values in shared memory: 256 and a
+                                 // pad that puts the tokens of a load phase on different banks
+constexpr int kPF = 2;           // units in flight per warp
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+
+// Eight E2M1 codes -> four FP16 pairs (elements 2i, 2i+1 in h[i]), exactly.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct Unit {
+    uint4 w[4];   // codes of rows 8o + g + 32 i, K = 32t .. 32t + 31
+    uint4 sf;     // their scale atom row: word i = row i's four scales of 64 elements
+};
+
+}  // namespace
+
+template <int NT>   // groups of 8 tokens
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) k_matvec_nvfp4(const MatvecParams p) {
+    extern __shared__ __align__(16) uint8_t mv_smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int S = p.splits, WK = p.wk;
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const int ncl = (int)gridDim.x / S, cl = (int)blockIdx.x / S;
+    const int nkb = p.nkb;                                   // K / 128
+    const int kb0 = (int)((int64_t)nkb * rank / S), kb1 = (int)((int64_t)nkb * (rank + 1) / S);
+    const int kslice = kb1 - kb0, kmax = (nkb + S - 1) / S;
+    uint8_t* xs = mv_smem;                                   // [kslice][M] blocks of kXBlock
+    float* inv = reinterpret_cast<float*>(mv_smem + (size_t)kmax * p.M * kXBlock);   // [kslice][8 NT]
+    float* red = inv + (size_t)kmax * 8 * NT;                // [kWarps][8 NT tokens][32 rows]
+
+    const int per = kWarps / WK;                             // tiles at a time
+    const int ntile = p.tiles;                               // N / 32
+    const int wt = warp / WK, wk = warp % WK;                // this warp's tile slot and K slot
+    const int my_units = kslice > wk ? (kslice - wk + WK - 1) / WK : 0;
+
+    // the sequence of units of this warp: tiles cl * per + wt, + ncl * per, ..; K-blocks wk, + WK, ..
+    int ld_tile = cl * per + wt, ld_u = 0;
+    auto load_unit = [&](Unit& u) {
+        while (ld_u >= my_units && ld_tile < ntile) {
+            ld_tile += ncl * per;
+            ld_u = 0;
+            if (my_units == 0) ld_tile = ntile;
+        }
+        if (ld_tile >= ntile) return;
+        const int kb = kb0 + wk + ld_u * WK;
+        const int64_t rg = ld_tile >> 2;
+        const int o8 = 8 * (ld_tile & 3) + g;                // row within the atom's 32
+        const uint8_t* w = p.qw + (rg * 128 + o8) * (int64_t)nkb * 64 + (int64_t)kb * 64 + 16 * t;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) u.w[i] = ldg_stream(w + (int64_t)i * 32 * nkb * 64);
+        u.sf = ldg_stream(p.sfw + (rg * nkb * 2 + 2 * kb + (t >> 1)) * 512 + o8 * 16);
+        ++ld_u;
+    };
+    Unit u[kPF];
+    #pragma unroll
+    for (int i = 0; i < kPF; ++i) load_unit(u[i]);
+
+    // x to FP16 in fragment order: 16 lanes take one (K-block, token) block of 128.  Lane l holds
+    // elements 8l .. 8l + 7, that is lane t = l / 4 of the MMA, quarter jj = l % 4: slot 4 jj + t.
+    {
+        const int l = tid & 15, items = kslice * p.M;
+        for (int it0 = (tid >> 5) * 2; it0 < items; it0 += 2 * kWarps) {
+            const int it = it0 + ((tid >> 4) & 1);
+            const bool act = it < items;
+            const int kb = act ? it / p.M : 0, m = act ? it - kb * p.M : 0;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (act) v = *reinterpret_cast<const uint4*>(p.x + (int64_t)m * p.ldx + (int64_t)(kb0 + kb) * 128 + 8 * l);
+            uint32_t mx = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+            mx = max(mx & 0xFFFFu, mx >> 16);
+            #pragma unroll
+            for (int off = 8; off >= 1; off >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            // biased exponent of the maximum, at least 15 so that both factors are normal numbers
+            const uint32_t e = max(mx >> 7, 15u);
+            const float f = __uint_as_float((268u - e) << 23);          // 2^(141 - e)
+            uint32_t h[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t wv = word(v, j);
+                const float lo = __uint_as_float(wv << 16) * f, hi = __uint_as_float(wv & 0xFFFF0000u) * f;
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(hi), "f"(lo));
+            }
+            if (act) {
+                *reinterpret_cast<uint4*>(xs + (size_t)it * kXBlock + (4 * (l & 3) + (l >> 2)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (l == 0) inv[kb * 8 * NT + m] = __uint_as_float((e - 14u) << 23);   // 2^(e - 141)
+            }
+        }
+        // tokens past M: their columns are zero
+        for (int i = tid; i < kslice * 8 * NT; i += kWarps * 32)
+            if (i % (8 * NT) >= p.M) inv[i] = 0.0f;
+    }
+    __syncthreads();
+
+    for (int tile0 = cl * per; tile0 < ntile; tile0 += ncl * per) {
+        const int tile = tile0 + wt;
+        float tot[NT][2][4];
+        #pragma unroll
+        for (int a = 0; a < NT; ++a)
+            #pragma unroll
+            for (int b = 0; b < 2; ++b)
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) tot[a][b][c] = 0.0f;
+        if (tile < ntile) {
+            for (int un = 0; un < my_units; ++un) {
+                const Unit cur = u[0];
+                #pragma unroll
+                for (int i = 0; i + 1 < kPF; ++i) u[i] = u[i + 1];
+                load_unit(u[kPF - 1]);
+                const int kb = wk + un * WK;
+                // scales of each row: groups 2t (K words 0, 1) and 2t + 1 (words 2, 3)
+                uint32_t s2[4][2];
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint16_t pr = (uint16_t)(word(cur.sf, i) >> (16 * (t & 1)));
+                    uint32_t h;
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(pr));
+                    s2[i][0] = __byte_perm(h, h, 0x1010);
+                    s2[i][1] = __byte_perm(h, h, 0x3232);
+                }
+                float acc[NT][2][4];
+                #pragma unroll
+                for (int a = 0; a < NT; ++a)
+                    #pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        #pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.0f;
+                #pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    uint4 b[NT];
+                    #pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        b[a] = make_uint4(0, 0, 0, 0);
+                        const int m = 8 * a + g;
+                        if (m < p.M) b[a] = *reinterpret_cast<const uint4*>(xs + ((size_t)kb * p.M + m) * kXBlock + (4 * jj + t) * 16);
+                    }
+                    #pragma unroll
+                    for (int T = 0; T < 2; ++T) {
+                        uint32_t ha[4], hb[4];
+                        e2m1x8(word(cur.w[2 * T], jj), ha);
+                        e2m1x8(word(cur.w[2 * T + 1], jj), hb);
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            ha[i] = hmul2(ha[i], s2[2 * T][jj >> 1]);
+                            hb[i] = hmul2(hb[i], s2[2 * T + 1][jj >> 1]);
+                        }
+                        #pragma unroll
+                        for (int a = 0; a < NT; ++a) {
+                            mma_f16(acc[a][T], ha[0], hb[0], ha[1], hb[1], b[a].x, b[a].y);
+                            mma_f16(acc[a][T], ha[2], hb[2], ha[3], hb[3], b[a].z, b[a].w);
+                        }
+                    }
+                }
+                #pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    const float2 iv = *reinterpret_cast<const float2*>(inv + kb * 8 * NT + 8 * a + 2 * t);
+                    #pragma unroll
+                    for (int T = 0; T < 2; ++T) {
+                        tot[a][T][0] = fmaf(acc[a][T][0], iv.x, tot[a][T][0]);
+                        tot[a][T][1] = fmaf(acc[a][T][1], iv.y, tot[a][T][1]);
+                        tot[a][T][2] = fmaf(acc[a][T][2], iv.x, tot[a][T][2]);
+                        tot[a][T][3] = fmaf(acc[a][T][3], iv.y, tot[a][T][3]);
+                    }
+                }
+            }
+        }
+        // parts to shared memory, [token][32 i + ... as 8 i + g]
+        #pragma unroll
+        for (int a = 0; a < NT; ++a)
+            #pragma unroll
+            for (int T = 0; T < 2; ++T)
+                #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    red[(warp * 8 * NT + 8 * a + 2 * t + (c & 1)) * 32 + 8 * (2 * T + (c >> 1)) + g] = tot[a][T][c];
+        if (S > 1) cluster_sync_all();
+        else __syncthreads();
+        // outputs of the `per` tiles, shared out over the cluster: the parts in order
+        const int n_out = per * p.M * 32;
+        for (int i = rank * kWarps * 32 + tid; i < n_out; i += S * kWarps * 32) {
+            const int r = i & 31, m = (i >> 5) % p.M, sl = (i >> 5) / p.M;
+            const int tl = tile0 + sl;
+            if (tl >= ntile) continue;
+            float v = 0.0f;
+            for (int s = 0; s < S; ++s) {
+                const uint32_t at = smem_u32(red + ((sl * WK) * 8 * NT + m) * 32 + r);
+                const uint32_t from = S > 1 ? mapa_shared(at, (uint32_t)s) : at;
+                for (int w = 0; w < WK; ++w) {
+                    float q;
+                    if (S > 1)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(from + (uint32_t)w * 8 * NT * 32 * 4) : "memory");
+                    else
+                        q = red[((sl * WK + w) * 8 * NT + m) * 32 + r];
+                    v += q;
+                }
+            }
+            const int64_t n = (int64_t)(tl >> 2) * 128 + 32 * (r >> 3) + 8 * (tl & 3) + (r & 7);
+            p.y[(int64_t)m * p.ldy + n] = (uint16_t)(pack_bf16x2(v * p.gw[n], 0.0f) & 0xFFFFu);
+        }
+        // the next tiles' parts (or the exit of a CTA whose parts are still read)
+        if (S > 1) cluster_sync_all();
+        else __syncthreads();
+    }
+}
+
+size_t matvec_smem(int M, int nkb, int splits) {
+    const int nt = (M + 7) / 8, kmax = (nkb + splits - 1) / splits;
+    return (size_t)kmax * M * kXBlock + (size_t)kmax * 8 * nt * 4 + (size_t)kWarps * 8 * nt * 32 * 4;
+}
+
+cudaError_t launch_matvec_nvfp4(const MatvecParams& p, int clusters, cudaStream_t st) {
+    const size_t smem = matvec_smem(p.M, p.nkb, p.splits);
+    auto kern = p.M <= 8 ? k_matvec_nvfp4<1> : k_matvec_nvfp4<2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * p.splits), 1, 1);
+    cfg.blockDim = dim3(kWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace fp8rl

@@ -625,3 +625,28 @@ def linear_nvfp4(x: torch.Tensor, qw, sfw, gw, out=None):
     check(lib().fp8rl_linear_nvfp4(_ptr(x), M, K, x.stride(0), _ptr(qw), _ptr(sfw), _ptr(gw), N, _ptr(qx),
                                    _ptr(sfx), _ptr(gx), _ptr(y), _stream(dev)), "fp8rl_linear_nvfp4")
     return y, qx, sfx, gx
+
+
+def matvec_nvfp4(x: torch.Tensor, qw: torch.Tensor, sfw: torch.Tensor, gw: torch.Tensor, out=None,
+                 splits: int = 0) -> torch.Tensor:
+    """y = X W^T bf16 [M,N] for 1 to 16 tokens, the activation x bf16 [M,K] unquantized and W in
+    NVFP4 (quantize_nvfp4's q, sf, g): weight-only 4-bit rollout.  `out` may be a [M,N] bf16
+    view with contiguous rows."""
+    _matrix(x, "x")
+    _require(x, torch.bfloat16, "x")
+    M, K = x.shape
+    dev = x.device
+    ldx = _rows(x, "x", (M, K), dev)
+    for t, n, dt in ((qw, "qw", torch.uint8), (sfw, "sfw", torch.uint8), (gw, "gw", torch.float32)):
+        _require(t, dt, n, dev)
+        _contig(t, n)
+    N = gw.numel()
+    if tuple(qw.shape) != (N, K // 2) or K % 2 != 0:
+        raise ValueError(f"qw: expected shape {(N, K // 2)}, got {tuple(qw.shape)}")
+    if N > 0 and sfw.numel() != nvfp4_scale_bytes(N, K):
+        raise ValueError(f"sfw: expected {nvfp4_scale_bytes(N, K)} bytes, got {sfw.numel()}")
+    y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    ldy = _rows(y, "out", (M, N), dev)
+    check(lib().fp8rl_matvec_nvfp4(_ptr(x), M, K, ldx, _ptr(qw), _ptr(sfw), _ptr(gw), N, _ptr(y), ldy,
+                                   int(splits), _stream(dev)), "fp8rl_matvec_nvfp4")
+    return y

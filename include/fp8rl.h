@@ -478,6 +478,21 @@ FP8RL_API fp8rl_status fp8rl_linear_nvfp4(const uint16_t* x, int64_t M, int64_t 
                                           int64_t N, uint8_t* qx, uint8_t* sfx, float* gx,
                                           uint16_t* y, fp8rl_stream_t stream);
 
+/* The same linear for 1 to 16 tokens with the activation left in BF16: only the weights are in
+ * 4 bits.  y[m][n] = bf16_rne(gw[n] sum_k x[m][k] w^(n,k)), w^ the code times its block scale;
+ * the products are exact (an element below 2^-28 of the largest of its 128 neighbours may lose
+ * bits) and are summed in FP32 in a fixed order.
+ *   x : BF16 [M][ldx], ldx >= K, ldx % 8 == 0;  qw / sfw / gw as fp8rl_quantize_nvfp4 of W [N][K];
+ *   y : BF16 [M][ldy], ldy >= N, ldy % 8 == 0.  0 <= M <= 16, N % 128 == 0, K % 256 == 0.
+ * splits: CTAs of a cluster that share the reduction (1..8; 0 = automatic).  A token's result
+ * may differ in its last bit between calls of different M.  No workspace, one launch
+ * (more only when K is so long that the tokens' x does not fit in shared memory at once:
+ * FP8RL_ERR_SHAPE when a single token's does not). */
+FP8RL_API fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
+                                          const uint8_t* qw, const uint8_t* sfw, const float* gw,
+                                          int64_t N, uint16_t* y, int64_t ldy, int splits,
+                                          fp8rl_stream_t stream);
+
 /* ----------------------------------------------------------------------------------------
  * Diagnostics (used by the tests).
  * -------------------------------------------------------------------------------------- */

@@ -60,3 +60,16 @@ def residual_norm_bwd(dz, dh, h, y, pre, r, post=None, rp=None, gate=None, alpha
         dm = rp * (um + yh.abs() * (um * yh.abs()).mean(1, keepdim=True))
     out["dy"] = (d, dm)
     return out
+
+
+def decode_nvfp4(q, sf, g):
+    """Values in 64 bits of NVFP4 rows: codes u8 [N,K/2], block scales in atoms of 128 rows x 4
+    (row r of an atom at byte 16 (r % 32) + 4 (r / 32)), row scales [N]; N % 128 == 0."""
+    N, K = q.shape[0], 2 * q.shape[1]
+    c = torch.stack([q & 15, q >> 4], 2).view(N, K).long()
+    table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=q.device)
+    w = table[c & 7] * torch.where(c > 7, -1.0, 1.0).double()
+    r, b = torch.arange(N, device=q.device)[:, None], torch.arange(K // 16, device=q.device)[None, :]
+    at = 512 * ((r // 128) * (K // 64) + b // 4) + 16 * (r % 32) + 4 * ((r % 128) // 32) + b % 4
+    scale = sf.view(torch.float8_e4m3fn)[at].double()
+    return w * scale.repeat_interleave(16, 1) * g.double()[:, None]

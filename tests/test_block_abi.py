@@ -89,3 +89,18 @@ def test_silu_checkpoint_refusals(abi, M, I, ptr, status):
     L = abi.lib()
     assert L.fp8rl_silu_mul_quant_ckpt(p["src"], M, I, p["q"], p["s"], p["qT"], p["sT"], p["ck"], p["sck"], None) == want
     assert L.fp8rl_silu_mul_bwd_quant_ckpt(p["ck"], p["sck"], p["src"], M, I, p["q"], p["s"], p["qT"], p["sT"], None) == want
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), "INVALID_ARG"), (dict(N=-1), "INVALID_ARG"), (dict(K=0), "INVALID_ARG"), (dict(ldx=128), "INVALID_ARG"),
+    (dict(ldy=64), "INVALID_ARG"), (dict(splits=-1), "INVALID_ARG"), (dict(splits=9), "INVALID_ARG"), (dict(M=17), "SHAPE"),
+    (dict(K=384, ldx=384), "SHAPE"), (dict(N=200, ldy=200), "SHAPE"), (dict(x=None), "INVALID_ARG"), (dict(q=None), "INVALID_ARG"),
+    (dict(sf=None), "INVALID_ARG"), (dict(g=None), "INVALID_ARG"), (dict(y=None), "INVALID_ARG"), (dict(x=ODD), "ALIGN"),
+    (dict(q=ODD), "ALIGN"), (dict(sf=ODD), "ALIGN"), (dict(g=ODD), "ALIGN"), (dict(y=ODD), "ALIGN"), (dict(ldx=260), "ALIGN"),
+    (dict(ldy=132), "ALIGN"), (dict(M=0, x=None, y=None), "OK"), (dict(N=0, q=None, ldy=0), "OK"),
+])
+def test_matvec_nvfp4_refusals(abi, kw, status):
+    a = {**dict(x=FAKE, M=4, K=256, ldx=256, q=FAKE, sf=FAKE, g=FAKE, N=128, y=FAKE, ldy=128, splits=0), **kw}
+    want = getattr(abi, "FP8RL_OK" if status == "OK" else f"FP8RL_ERR_{status}")
+    assert abi.lib().fp8rl_matvec_nvfp4(a["x"], a["M"], a["K"], a["ldx"], a["q"], a["sf"], a["g"], a["N"], a["y"], a["ldy"],
+                                        a["splits"], None) == want
