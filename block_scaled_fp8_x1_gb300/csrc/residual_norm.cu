@@ -29,34 +29,48 @@ __device__ __forceinline__ float elem(const uint4& v, int j) {
     return (j & 1) ? bf16_hi(w) : bf16_lo(w);
 }
 
-// Sum of one value per thread over the CTA, the same in every thread: a shuffle tree, then the
-// warps' sums in order.  Successive calls alternate between two buffers: a buffer is written
-// again only after the barrier of the call in between, which every reader has reached.
-__device__ __forceinline__ float block_sum(float v, float* buf, int nwarps) {
+// Sum of one value per thread over the CTA, the same in every thread: a shuffle tree in each
+// warp, then one over the warps' sums (buf[w], zero from nwarps up to 32).  Successive calls
+// alternate between two buffers: a buffer is written again only after the barrier of the call in
+// between, which every reader has reached.
+__device__ __forceinline__ float warp_sum(float v) {
     #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+    v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < nwarps; ++w) s += buf[w];
-    return s;
+    return warp_sum(buf[threadIdx.x & 31]);
 }
 
-// 1x128 codes of a row: thread t holds columns 8t .. 8t + 7, so a group is 16 lanes.  The words
-// are BF16 pairs; every lane of the warp takes part.
+__device__ __forceinline__ float2 pair(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+
+// Codes of four pairs of a group whose scale is too small for the division-free encode.
+__device__ __noinline__ uint2 encode8_slow(uint4 v, float s) {
+    uint32_t c[4];
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = e4m3x2(__fdiv_rn(bf16_lo(word(v, j)), s), __fdiv_rn(bf16_hi(word(v, j)), s));
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// 1x128 codes of a row: thread t holds 8 columns of BF16 pairs, so a group is 16 lanes.  Every
+// lane of the warp takes part.
 __device__ __forceinline__ void quant_row(const uint4& v, bool act, uint8_t* q, float* s) {
     uint32_t mx = absmax2(absmax2(absmax2(absmax2(0u, v.x), v.y), v.z), v.w);
     mx = max(mx & 0xFFFFu, mx >> 16);
     #pragma unroll
     for (int off = 8; off >= 1; off >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     if (!act) return;
-    const GroupScale gs = make_scale(bf16_bits_amax_to_f32(mx));
-    const uint32_t c0 = encode_pair(bf16_lo(v.x), bf16_hi(v.x), gs);
-    const uint32_t c1 = encode_pair(bf16_lo(v.y), bf16_hi(v.y), gs);
-    const uint32_t c2 = encode_pair(bf16_lo(v.z), bf16_hi(v.z), gs);
-    const uint32_t c3 = encode_pair(bf16_lo(v.w), bf16_hi(v.w), gs);
-    *reinterpret_cast<uint2*>(q) = make_uint2(c0 | (c1 << 16), c2 | (c3 << 16));
-    if ((threadIdx.x & 15) == 0) *s = gs.s;
+    const FastScale f = fast_scale(bf16_bits_amax_to_f32(mx));
+    uint2 c = make_uint2(flip_codes(encode_pair_neg(pair(v.x), f.s, f.nr), encode_pair_neg(pair(v.y), f.s, f.nr), f.keep),
+                         flip_codes(encode_pair_neg(pair(v.z), f.s, f.nr), encode_pair_neg(pair(v.w), f.s, f.nr), f.keep));
+    if (f.slow) c = encode8_slow(v, f.s);
+    *reinterpret_cast<uint2*>(q) = c;
+    if ((threadIdx.x & 15) == 0) *s = f.s;
 }
 
 __device__ __forceinline__ float rstd_of(float sumsq, float k, float eps) {
@@ -65,79 +79,121 @@ __device__ __forceinline__ float rstd_of(float sumsq, float k, float eps) {
 
 }  // namespace
 
-// One row per CTA at a time, thread t on columns 8t .. 8t + 7 (K <= 8192: up to 1024 threads).
-// The layout depends on K alone, so a token's row has the same bits alone and in a batch.
-template <bool POST>
-__global__ void __launch_bounds__(1024, 1) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
+// One row per CTA at a time; thread t holds columns 8 (t + NT i), i < NCH.  The next row's words
+// are requested before this row is reduced.  The layout depends on K alone, so a token's row has
+// the same bits alone and in a batch.
+template <bool POST, int NCH>
+__global__ void __launch_bounds__(512, 2) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
+    extern __shared__ __align__(16) float s_w[];      // alpha * gate * g_post [K]
     __shared__ float s_sum[2][32];
-    const int tid = threadIdx.x, nwarps = blockDim.x >> 5;
-    const int64_t c = 8 * (int64_t)tid;
-    const bool act = c < K;
+    const int tid = threadIdx.x, nt = blockDim.x;
     const float kf = (float)K;
     int par = 0;
-    // alpha * gate * g_post, and g_pre as BF16 pairs
-    float w[8];
-    uint4 pre = make_uint4(0, 0, 0, 0);
-    {
+    uint4 pre[NCH];
+    #pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int c = 8 * (tid + nt * i);
         const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-        const uint4 g = act && a.gate ? ld_v4(a.gate + c) : one;
-        const uint4 p = act && POST ? ld_v4(a.post_gamma + c) : one;
-        if (act) pre = ld_v4(a.pre_gamma + c);
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = a.alpha * elem(g, j) * elem(p, j);
-    }
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-        uint4 hv = make_uint4(0, 0, 0, 0), yv = make_uint4(0, 0, 0, 0);
-        if (act) {
-            hv = ld_v4(a.h + m * a.ldh + c);
-            yv = ld_v4(a.y + m * a.ldy + c);
+        pre[i] = make_uint4(0, 0, 0, 0);
+        if (c < K) {
+            const uint4 g = a.gate ? ld_v4(a.gate + c) : one;
+            const uint4 p = POST ? ld_v4(a.post_gamma + c) : one;
+            pre[i] = ld_v4(a.pre_gamma + c);
+            #pragma unroll
+            for (int j = 0; j < 8; ++j) s_w[c + j] = a.alpha * elem(g, j) * elem(p, j);
         }
+    }
+    if (tid < 32) s_sum[0][tid] = s_sum[1][tid] = 0.0f;
+    __syncthreads();
+    uint4 nh[NCH], ny[NCH];
+    auto load_row = [&](int64_t m) {
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = 8 * (tid + nt * i);
+            nh[i] = ny[i] = make_uint4(0, 0, 0, 0);
+            if (c < K && m < M) {
+                nh[i] = ld_v4(a.h + m * a.ldh + c);
+                ny[i] = ld_v4(a.y + m * a.ldy + c);
+            }
+        }
+    };
+    load_row(blockIdx.x);
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        uint4 hv[NCH], yv[NCH];
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            hv[i] = nh[i];
+            yv[i] = ny[i];
+        }
+        load_row(m + gridDim.x);
         float ry = 1.0f;
         if (POST) {
-            float ss = 0.0f;
+            float2 ss = both(0.0f);
             #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(elem(yv, j), elem(yv, j), ss);
-            ry = rstd_of(block_sum(ss, s_sum[par], nwarps), kf, a.eps);
+            for (int i = 0; i < NCH; ++i)
+                #pragma unroll
+                for (int j = 0; j < 4; ++j) ss = __ffma2_rn(pair(word(yv[i], j)), pair(word(yv[i], j)), ss);
+            ry = rstd_of(block_sum(ss.x + ss.y, s_sum[par]), kf, a.eps);
             par ^= 1;
         }
-        uint32_t o[4];
+        float2 ss = both(0.0f);
         #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = pack_bf16x2(fmaf(elem(yv, 2 * j) * ry, w[2 * j], elem(hv, 2 * j)),
-                               fmaf(elem(yv, 2 * j + 1) * ry, w[2 * j + 1], elem(hv, 2 * j + 1)));
-        const uint4 hn = make_uint4(o[0], o[1], o[2], o[3]);
-        float ss = 0.0f;
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(elem(hn, j), elem(hn, j), ss);
-        const float r = rstd_of(block_sum(ss, s_sum[par], nwarps), kf, a.eps);
+        for (int i = 0; i < NCH; ++i) {
+            const int c = 8 * (tid + nt * i);
+            uint32_t o[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 w = c < K ? *reinterpret_cast<const float2*>(s_w + c + 2 * j) : both(0.0f);
+                const float2 x = __ffma2_rn(__fmul2_rn(pair(word(yv[i], j)), both(ry)), w, pair(word(hv[i], j)));
+                o[j] = pack_bf16x2(x.x, x.y);
+                ss = __ffma2_rn(pair(o[j]), pair(o[j]), ss);
+            }
+            hv[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        const float r = rstd_of(block_sum(ss.x + ss.y, s_sum[par]), kf, a.eps);
         par ^= 1;
-        #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = pack_bf16x2(__fmul_rn(__fmul_rn(elem(hn, 2 * j), r), elem(pre, 2 * j)),
-                               __fmul_rn(__fmul_rn(elem(hn, 2 * j + 1), r), elem(pre, 2 * j + 1)));
-        const uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
-        if (act) *reinterpret_cast<uint4*>(a.h_out + m * K + c) = hn;
         if (tid == 0) {
             a.r_pre[m] = r;
             if (POST) a.r_post[m] = ry;
         }
-        const int64_t sc = (c >> 7) * M + m;
-        if (a.z && act) *reinterpret_cast<uint4*>(a.z + m * K + c) = z;
-        if (a.q) quant_row(z, act, a.q + m * K + c, a.s + sc);
-        if (a.qh) quant_row(hn, act, a.qh + m * K + c, a.sh + sc);
-        if (a.qy) quant_row(yv, act, a.qy + m * K + c, a.sy + sc);
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = 8 * (tid + nt * i);
+            const bool act = c < K;
+            uint32_t o[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = __fmul2_rn(__fmul2_rn(pair(word(hv[i], j)), both(r)), pair(word(pre[i], j)));
+                o[j] = pack_bf16x2(x.x, x.y);
+            }
+            const uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
+            if (act) *reinterpret_cast<uint4*>(a.h_out + m * K + c) = hv[i];
+            const int64_t sc = (int64_t)(c >> 7) * M + m;
+            if (a.z && act) *reinterpret_cast<uint4*>(a.z + m * K + c) = z;
+            if (a.q) quant_row(z, act, a.q + m * K + c, a.s + sc);
+            if (a.qh) quant_row(hv[i], act, a.qh + m * K + c, a.sh + sc);
+            if (a.qy) quant_row(yv[i], act, a.qy + m * K + c, a.sy + sc);
+        }
     }
 }
 
 static int norm_threads(int64_t K) { return (int)((K / 8 + 31) / 32 * 32); }
 
-cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
-    const int nt = norm_threads(K);
-    const int64_t grid = (int64_t)num_sms * (2048 / nt > 16 ? 16 : 2048 / nt);
-    const unsigned g = (unsigned)(M < grid ? M : grid);
-    if (a.post_gamma) k_residual_norm<true><<<g, nt, 0, st>>>(a, M, K);
-    else k_residual_norm<false><<<g, nt, 0, st>>>(a, M, K);
+template <int NCH>
+static cudaError_t launch_fwd_t(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
+    const int nt = norm_threads((K / 8 + NCH - 1) / NCH * 8);
+    auto kern = a.post_gamma ? k_residual_norm<true, NCH> : k_residual_norm<false, NCH>;
+    int per_sm = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, (size_t)K * 4);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+    kern<<<(unsigned)(M < grid ? M : grid), nt, (size_t)K * 4, st>>>(a, M, K);
     return cudaGetLastError();
+}
+
+cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
+    if (K <= 4096) return launch_fwd_t<1>(a, M, K, num_sms, st);
+    return launch_fwd_t<2>(a, M, K, num_sms, st);
 }
 
 // ------------------------------------------------------------------------------------ backward
@@ -196,7 +252,9 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
     k_residual_norm_bwd(const fp8rl_residual_norm_bwd_args a, int64_t M, int64_t K, float* __restrict__ ws) {
     constexpr bool NEED_Y = POST || GATE;
     __shared__ float s_sum[2][32];
-    const int tid = threadIdx.x, nt = blockDim.x, nwarps = nt >> 5;
+    const int tid = threadIdx.x, nt = blockDim.x;
+    if (tid < 32) s_sum[0][tid] = s_sum[1][tid] = 0.0f;
+    __syncthreads();
     const int64_t rows = (M + gridDim.x - 1) / gridDim.x;
     const int64_t m0 = (int64_t)blockIdx.x * rows;
     const int64_t m1 = m0 + rows < M ? m0 + rows : M;
@@ -237,7 +295,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
             #pragma unroll
             for (int j = 0; j < 8; ++j) part = fmaf(elem(dzv[i], j) * elem(pre[i], j), x[j] * r, part);
         }
-        const float mean1 = block_sum(part, s_sum[par], nwarps) * inv_k;
+        const float mean1 = block_sum(part, s_sum[par]) * inv_k;
         par ^= 1;
         float u[NCH][8];
         part = 0.0f;
@@ -272,7 +330,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
         }
         float mean2 = 0.0f;
         if (POST) {
-            mean2 = block_sum(part, s_sum[par], nwarps) * inv_k;
+            mean2 = block_sum(part, s_sum[par]) * inv_k;
             par ^= 1;
         }
         #pragma unroll
