@@ -749,7 +749,7 @@ size_t fp8rl_residual_norm_bwd_workspace_bytes(int64_t M, int64_t K) {
     if (M <= 0 || K <= 0 || K % 128 != 0 || K > kResNormMaxK) return 0;
     int sms = 0;
     if (current_device(&sms) != FP8RL_OK) sms = 152;
-    return (size_t)residual_norm_bwd_blocks(M, K, sms) * 3 * (size_t)K * sizeof(float);
+    return (size_t)residual_norm_bwd_blocks(M, K, true, sms) * 2 * (size_t)K * sizeof(float);
 }
 
 fp8rl_status fp8rl_residual_norm_bwd(const fp8rl_residual_norm_bwd_args* args, int64_t M, int64_t K, void* ws,
@@ -785,8 +785,8 @@ fp8rl_status fp8rl_residual_norm_bwd(const fp8rl_residual_norm_bwd_args* args, i
     int sms = 0;
     e = current_device(&sms);
     if (e != FP8RL_OK) return e;
-    const int nblocks = residual_norm_bwd_blocks(M, K, sms);
-    if (!ws || ws_bytes < (size_t)nblocks * 3 * (size_t)K * sizeof(float)) return FP8RL_ERR_WORKSPACE;
+    const int nblocks = residual_norm_bwd_blocks(M, K, a.qh != nullptr, sms);
+    if (!ws || ws_bytes < (size_t)nblocks * 2 * (size_t)K * sizeof(float)) return FP8RL_ERR_WORKSPACE;
     if (!aligned16(ws)) return FP8RL_ERR_ALIGN;
     return cuda_status(launch_residual_norm_bwd(a, M, K, reinterpret_cast<float*>(ws), nblocks, stream));
 }

@@ -12,7 +12,9 @@ namespace fp8rl {
 constexpr int64_t kResNormMaxK = 8192;
 
 cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st);
-int residual_norm_bwd_blocks(int64_t M, int64_t K, int num_sms);
+// Row blocks of the backward; a row of checkpoints takes less shared memory, so no form has more
+// blocks than that one.
+int residual_norm_bwd_blocks(int64_t M, int64_t K, bool ckpt, int num_sms);
 cudaError_t launch_residual_norm_bwd(const fp8rl_residual_norm_bwd_args& a, int64_t M, int64_t K, float* ws,
                                      int nblocks, cudaStream_t st);
 

@@ -200,206 +200,297 @@ cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, i
 
 namespace {
 
-// Eight saved values: BF16 words, or E4M3 codes times their group's scale.
-struct Saved8 {
-    uint4 w;      // BF16 pairs, or the eight codes in x, y
-    float s;
+// One row's words of a thread's chunk of 8 columns, as they lie in its slot of shared memory:
+// dz and dh (BF16), then h' and y (BF16, or E4M3 codes and their group's scale).  A thread copies
+// and reads only its own chunks, so the copies need no barrier, only its own wait.
+template <bool CK>
+struct Slot {
+    static constexpr int SAVED = CK ? 8 : 16;
+    static constexpr int BYTES = 32 + 2 * SAVED + (CK ? 8 : 0);   // a chunk of one thread
 };
-template <bool CK>
-__device__ __forceinline__ void saved_values(const Saved8& v, float (&x)[8]) {
-    if (!CK) {
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = elem(v.w, j);
-        return;
-    }
-    #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint16_t pair = (uint16_t)((j < 2 ? v.w.x : v.w.y) >> (16 * (j & 1)));
-        float d0, d1;
-        asm("{\n\t.reg .b32 h;\n\t.reg .f16 a, b;\n\t"
-            "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
-            "mov.b32 {a, b}, h;\n\t"
-            "cvt.f32.f16 %0, a;\n\t"
-            "cvt.f32.f16 %1, b;\n\t}"
-            : "=f"(d0), "=f"(d1)
-            : "h"(pair));
-        x[2 * j] = d0 * v.s;
-        x[2 * j + 1] = d1 * v.s;
-    }
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
-template <bool CK>
-__device__ __forceinline__ Saved8 load_saved(const uint16_t* x, int64_t ld, const uint8_t* q, const float* s, int64_t m,
-                                             int64_t c, int64_t M, int64_t K) {
-    Saved8 v;
-    v.s = 0.0f;
-    if (CK) {
-        const uint2 w = *reinterpret_cast<const uint2*>(q + m * K + c);
-        v.w = make_uint4(w.x, w.y, 0, 0);
-        v.s = s[(c >> 7) * M + m];
-    } else {
-        v.w = ld_v4(x + m * ld + c);
-    }
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// Two E4M3 codes to FP32, exactly: through FP16, which holds every finite E4M3.
+__device__ __forceinline__ float2 e4m3_pair(uint32_t codes) {
+    float2 d;
+    asm("{\n\t.reg .b32 h;\n\t.reg .f16 a, b;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
+        "mov.b32 {a, b}, h;\n\t"
+        "cvt.f32.f16 %0, a;\n\t"
+        "cvt.f32.f16 %1, b;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "h"((uint16_t)codes));
+    return d;
+}
+
+// Eight saved values times f (and times the checkpoint's scale).
+template <bool CK>
+__device__ __forceinline__ void saved_times(uint32_t words, uint32_t scale, float f, float2 (&x)[4]) {
+    if (CK) {
+        const uint2 c = lds_v2(words);
+        const float2 k = both(lds_f32(scale) * f);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(e4m3_pair((j < 2 ? c.x : c.y) >> (16 * (j & 1))), k);
+    } else {
+        const uint4 w = lds_v4(words);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(pair(word(w, j)), both(f));
+    }
 }
 
 }  // namespace
 
-// Row block b of the grid takes rows [b rows, (b+1) rows).  Thread t holds columns 8 (t + NT i),
-// i < NCH; its shares of the column sums stay in registers over the rows and go to
-// ws[b][0..2][K] (g_pre, g_post, gate), which k_resnorm_colsum adds in block order.
+// Row block b of the grid takes rows [b rows, (b+1) rows); thread t holds columns 8 (t + NT i),
+// i < NCH.  The rows ahead (SLOTS - 1 of them) are copied to shared memory meanwhile.
+//
+// With w = alpha gate g_post, u = w dH and v = dH y^: mean(u y^) = mean(w v), and the two column
+// sums over the branch are multiples of one, V = sum_m v: dgate = alpha g_post V and
+// dg_post = alpha gate V.  So a thread keeps two sums for a column, dg_pre and V, in registers over
+// its rows; ws[b][0..1][K] takes them, and k_resnorm_colsum adds the blocks in order.
 template <bool POST, bool GATE, bool CK, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
-    k_residual_norm_bwd(const fp8rl_residual_norm_bwd_args a, int64_t M, int64_t K, float* __restrict__ ws) {
+    k_residual_norm_bwd(const fp8rl_residual_norm_bwd_args a, int64_t M, int64_t K, int slots, float* __restrict__ ws) {
     constexpr bool NEED_Y = POST || GATE;
+    using SL = Slot<CK>;
+    extern __shared__ __align__(16) uint8_t rn_smem[];
     __shared__ float s_sum[2][32];
     const int tid = threadIdx.x, nt = blockDim.x;
     if (tid < 32) s_sum[0][tid] = s_sum[1][tid] = 0.0f;
-    __syncthreads();
     const int64_t rows = (M + gridDim.x - 1) / gridDim.x;
     const int64_t m0 = (int64_t)blockIdx.x * rows;
     const int64_t m1 = m0 + rows < M ? m0 + rows : M;
     const float inv_k = __fdiv_rn(1.0f, (float)K);
     int par = 0;
-    uint4 pre[NCH], post[NCH], gate[NCH];
-    float a_pre[NCH][8], a_post[NCH][8], a_gate[NCH][8];
+    // slot layout: for each chunk index i, arrays over the threads of dz, dh, h', y (and scales)
+    const uint32_t base = smem_u32(rn_smem);
+    const uint32_t chunk = (uint32_t)nt * SL::BYTES, slot_bytes = chunk * NCH;
+    auto at = [&](int slot, int i, int what) -> uint32_t {   // 0 dz, 1 dh, 2 h', 3 y, 4 sh, 5 sy
+        const uint32_t b = base + (uint32_t)slot * slot_bytes + (uint32_t)i * chunk;
+        if (what < 2) return b + (uint32_t)(what * nt + tid) * 16u;
+        if (what < 4) return b + (uint32_t)nt * 32u + (uint32_t)((what - 2) * nt + tid) * SL::SAVED;
+        return b + (uint32_t)nt * (32u + 2u * SL::SAVED) + (uint32_t)((what - 4) * nt + tid) * 4u;
+    };
+    auto copy_row = [&](int64_t m, int slot) {
+        if (m < m1) {
+            #pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int64_t c = 8 * (int64_t)(tid + nt * i);
+                if (c >= K) continue;
+                cp_async_16(at(slot, i, 0), a.dz + m * a.lddz + c);
+                if (a.dh) cp_async_16(at(slot, i, 1), a.dh + m * a.lddh + c);
+                if (CK) {
+                    cp_async_8(at(slot, i, 2), a.qh + m * K + c);
+                    cp_async_4(at(slot, i, 4), a.sh + (c >> 7) * M + m, 4);
+                    if (NEED_Y) {
+                        cp_async_8(at(slot, i, 3), a.qy + m * K + c);
+                        cp_async_4(at(slot, i, 5), a.sy + (c >> 7) * M + m, 4);
+                    }
+                } else {
+                    cp_async_16(at(slot, i, 2), a.h + m * a.ldh + c);
+                    if (NEED_Y) cp_async_16(at(slot, i, 3), a.y + m * a.ldy + c);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    // a thread's chunks past K, and dh where there is none, stay zero
+    for (int sl = 0; sl < slots; ++sl)
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const bool in = 8 * (int64_t)(tid + nt * i) < K;
+            if (!in || !a.dh) st_shared_v4(at(sl, i, 1), make_uint4(0, 0, 0, 0));
+            if (!in) {
+                st_shared_v4(at(sl, i, 0), make_uint4(0, 0, 0, 0));
+                #pragma unroll
+                for (int w = 2; w < 4; ++w)
+                    #pragma unroll
+                    for (int o = 0; o < SL::SAVED; o += 4) st_shared_b32(at(sl, i, w) + o, 0);
+                if (CK) {
+                    st_shared_b32(at(sl, i, 4), 0);
+                    st_shared_b32(at(sl, i, 5), 0);
+                }
+            }
+        }
+    for (int sl = 0; sl < slots - 1; ++sl) copy_row(m0 + sl, sl);
+
+    uint4 pre[NCH];
+    float2 w[NCH][4], a_pre[NCH][4], a_v[NCH][4];
     #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int64_t c = 8 * (int64_t)(tid + nt * i);
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        pre[i] = c < K ? ld_v4(a.pre_gamma + c) : zero;
-        post[i] = POST && c < K ? ld_v4(a.post_gamma + c) : zero;
-        gate[i] = GATE && c < K ? ld_v4(a.gate + c) : zero;
+        const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        pre[i] = c < K ? ld_v4(a.pre_gamma + c) : make_uint4(0, 0, 0, 0);
+        const uint4 p = POST && c < K ? ld_v4(a.post_gamma + c) : one;
+        const uint4 g = GATE && c < K ? ld_v4(a.gate + c) : one;
         #pragma unroll
-        for (int j = 0; j < 8; ++j) a_pre[i][j] = a_post[i][j] = a_gate[i][j] = 0.0f;
-    }
-    for (int64_t m = m0; m < m1; ++m) {
-        const float r = a.r_pre[m];
-        const float ry = POST ? a.r_post[m] : 1.0f;
-        uint4 dzv[NCH], dhv[NCH];
-        Saved8 hv[NCH], yv[NCH];
-        float part = 0.0f;
-        #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int64_t c = 8 * (int64_t)(tid + nt * i);
-            dzv[i] = dhv[i] = make_uint4(0, 0, 0, 0);
-            hv[i].w = yv[i].w = make_uint4(0, 0, 0, 0);
-            hv[i].s = yv[i].s = 0.0f;
-            if (c < K) {
-                dzv[i] = ld_v4(a.dz + m * a.lddz + c);
-                if (a.dh) dhv[i] = ld_v4(a.dh + m * a.lddh + c);
-                hv[i] = load_saved<CK>(a.h, a.ldh, a.qh, a.sh, m, c, M, K);
-                if (NEED_Y) yv[i] = load_saved<CK>(a.y, a.ldy, a.qy, a.sy, m, c, M, K);
-            }
-            float x[8];
-            saved_values<CK>(hv[i], x);
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) part = fmaf(elem(dzv[i], j) * elem(pre[i], j), x[j] * r, part);
+        for (int j = 0; j < 4; ++j) {
+            w[i][j] = __fmul2_rn(__fmul2_rn(both(a.alpha), pair(word(g, j))), pair(word(p, j)));
+            a_pre[i][j] = a_v[i][j] = both(0.0f);
         }
-        const float mean1 = block_sum(part, s_sum[par]) * inv_k;
+    }
+    float r_next = m0 < m1 ? a.r_pre[m0] : 0.0f, ry_next = POST && m0 < m1 ? a.r_post[m0] : 1.0f;
+    __syncthreads();   // s_sum is zero
+    int slot = 0;
+    for (int64_t m = m0; m < m1; ++m) {
+        const float r = r_next, ry = ry_next;
+        if (m + 1 < m1) {
+            r_next = a.r_pre[m + 1];
+            if (POST) ry_next = a.r_post[m + 1];
+        }
+        // this row's copies have landed when at most the slots - 2 later ones are in flight
+        if (slots == 4) cp_async_wait_group<2>();
+        else cp_async_wait_group<1>();
+        float2 x[NCH][4], t[NCH][4], part = both(0.0f);
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            saved_times<CK>(at(slot, i, 2), at(slot, i, 4), r, x[i]);
+            const uint4 dz = lds_v4(at(slot, i, 0));
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 d = pair(word(dz, j));
+                t[i][j] = __fmul2_rn(d, pair(word(pre[i], j)));
+                part = __ffma2_rn(t[i][j], x[i][j], part);
+                a_pre[i][j] = __ffma2_rn(d, x[i][j], a_pre[i][j]);
+            }
+        }
+        const float mean1 = block_sum(part.x + part.y, s_sum[par]) * inv_k;
         par ^= 1;
-        float u[NCH][8];
-        part = 0.0f;
+        // every thread is past the row before: its slot takes the row slots - 1 ahead
+        copy_row(m + slots - 1, slot == 0 ? slots - 1 : slot - 1);
+        float2 y[NCH][4];
+        part = both(0.0f);
         #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int64_t c = 8 * (int64_t)(tid + nt * i);
-            float x[8], y[8], dH[8];
-            saved_values<CK>(hv[i], x);
-            if (NEED_Y) saved_values<CK>(yv[i], y);
+            const uint4 dh = lds_v4(at(slot, i, 1));
+            if (NEED_Y) saved_times<CK>(at(slot, i, 3), at(slot, i, 5), POST ? ry : 1.0f, y[i]);
+            uint32_t o[4];
             #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xh = x[j] * r, dz = elem(dzv[i], j);
-                a_pre[i][j] = fmaf(dz, xh, a_pre[i][j]);
-                dH[j] = fmaf(r, fmaf(-xh, mean1, dz * elem(pre[i], j)), elem(dhv[i], j));
-                float d = a.alpha * dH[j];
-                const float yh = NEED_Y ? (POST ? y[j] * ry : y[j]) : 0.0f;
-                if (GATE) {
-                    a_gate[i][j] = fmaf(d, POST ? yh * elem(post[i], j) : yh, a_gate[i][j]);
-                    d *= elem(gate[i], j);
+            for (int j = 0; j < 4; ++j) {
+                const float2 dH = __ffma2_rn(both(r), __ffma2_rn(x[i][j], both(-mean1), t[i][j]), pair(word(dh, j)));
+                o[j] = pack_bf16x2(dH.x, dH.y);
+                t[i][j] = __fmul2_rn(dH, w[i][j]);
+                if (NEED_Y) {
+                    const float2 v = __fmul2_rn(dH, y[i][j]);
+                    a_v[i][j] = __fadd2_rn(a_v[i][j], v);
+                    if (POST) part = __ffma2_rn(v, w[i][j], part);
                 }
-                if (POST) {
-                    a_post[i][j] = fmaf(d, yh, a_post[i][j]);
-                    d *= elem(post[i], j);
-                    part = fmaf(d, yh, part);
-                }
-                u[i][j] = d;
             }
-            if (c < K)
-                *reinterpret_cast<uint4*>(a.dh_out + m * K + c) =
-                    make_uint4(pack_bf16x2(dH[0], dH[1]), pack_bf16x2(dH[2], dH[3]), pack_bf16x2(dH[4], dH[5]),
-                               pack_bf16x2(dH[6], dH[7]));
+            if (c < K) *reinterpret_cast<uint4*>(a.dh_out + m * K + c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         float mean2 = 0.0f;
         if (POST) {
-            mean2 = block_sum(part, s_sum[par]) * inv_k;
+            mean2 = block_sum(part.x + part.y, s_sum[par]) * inv_k;
             par ^= 1;
         }
         #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int64_t c = 8 * (int64_t)(tid + nt * i);
-            if (POST) {
-                float y[8];
-                saved_values<CK>(yv[i], y);
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) u[i][j] = ry * fmaf(-(y[j] * ry), mean2, u[i][j]);
+            uint32_t o[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 d = t[i][j];
+                if (POST) d = __fmul2_rn(both(ry), __ffma2_rn(y[i][j], both(-mean2), d));
+                o[j] = pack_bf16x2(d.x, d.y);
             }
-            if (c < K)
-                *reinterpret_cast<uint4*>(a.dy + m * K + c) =
-                    make_uint4(pack_bf16x2(u[i][0], u[i][1]), pack_bf16x2(u[i][2], u[i][3]),
-                               pack_bf16x2(u[i][4], u[i][5]), pack_bf16x2(u[i][6], u[i][7]));
+            if (c < K) *reinterpret_cast<uint4*>(a.dy + m * K + c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        slot = slot + 1 == slots ? 0 : slot + 1;
     }
+    cp_async_wait_all();
     #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int64_t c = 8 * (int64_t)(tid + nt * i);
         if (c >= K) continue;
-        float* dst = ws + (int64_t)blockIdx.x * 3 * K + c;
+        float* dst = ws + (int64_t)blockIdx.x * 2 * K + c;
         #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            dst[j] = a_pre[i][j];
-            if (POST) dst[K + j] = a_post[i][j];
-            if (GATE) dst[2 * K + j] = a_gate[i][j];
+        for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<float2*>(dst + 2 * j) = a_pre[i][j];
+            if (NEED_Y) *reinterpret_cast<float2*>(dst + K + 2 * j) = a_v[i][j];
         }
     }
 }
 
 // Column sums over the row blocks: 32 columns by 8 slices of the blocks per CTA, each slice in
 // block order, then the slices in order.
-__global__ void __launch_bounds__(256) k_resnorm_colsum(const float* __restrict__ ws, int nblocks, int64_t K,
-                                                        float* dpre, float* dpost, float* dgate) {
+__global__ void __launch_bounds__(256) k_resnorm_colsum(const fp8rl_residual_norm_bwd_args a, const float* __restrict__ ws,
+                                                        int nblocks, int64_t K) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the rows are still worked on
     __shared__ float part[8][33];
     const int x = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t k = (int64_t)blockIdx.x * 32 + x;
-    float* out = blockIdx.y == 0 ? dpre : blockIdx.y == 1 ? dpost : dgate;
-    if (!out) return;
     float s = 0.0f;
-    for (int b = sl; b < nblocks; b += 8) s += ws[((int64_t)b * 3 + blockIdx.y) * K + k];
+    #pragma unroll 8
+    for (int b = sl; b < nblocks; b += 8) s += ws[((int64_t)b * 2 + blockIdx.y) * K + k];
     part[sl][x] = s;
     __syncthreads();
-    if (sl == 0) {
-        for (int i = 1; i < 8; ++i) s += part[i][x];
-        out[k] = s;
+    if (sl != 0) return;
+    for (int i = 1; i < 8; ++i) s += part[i][x];
+    if (blockIdx.y == 0) {
+        a.dpre[k] = s;
+        return;
     }
+    const float p = a.post_gamma ? bf16_bits_to_f32(a.post_gamma[k]) : 1.0f;
+    const float g = a.gate ? bf16_bits_to_f32(a.gate[k]) : 1.0f;
+    if (a.post_gamma) a.dpost[k] = a.alpha * g * s;
+    if (a.gate) a.dgate[k] = a.alpha * p * s;
 }
 
-static int bwd_nch(int64_t K) { return K <= 8 * 640 ? 1 : 2; }
+// Launch shape: one chunk of 8 columns a thread up to 640 threads (two above, whose sums and
+// constants would not fit the registers of 1024 threads), the ring's slots, CTAs per SM.
+struct BwdShape {
+    int nch, nt, slots, per_sm;
+    size_t smem;
+};
+static BwdShape bwd_shape(int64_t K, bool ck) {
+    BwdShape s;
+    s.nch = K <= 8 * 640 ? 1 : 2;
+    s.nt = norm_threads((K / 8 + s.nch - 1) / s.nch * 8);
+    const size_t row = (size_t)s.nt * s.nch * (ck ? Slot<true>::BYTES : Slot<false>::BYTES);
+    s.slots = 4 * row <= 200 * 1024 ? 4 : 3;
+    s.smem = (size_t)s.slots * row;
+    s.per_sm = (s.nch == 1 ? 640 : 512) / s.nt;
+    const int by_smem = (int)(216 * 1024 / (s.smem + 1536));
+    if (s.per_sm > by_smem) s.per_sm = by_smem;
+    if (s.per_sm > 8) s.per_sm = 8;
+    if (s.per_sm < 1) s.per_sm = 1;
+    return s;
+}
 
-int residual_norm_bwd_blocks(int64_t M, int64_t K, int num_sms) {
-    const int nch = bwd_nch(K);
-    const int nt = norm_threads((K / nch + 127) / 128 * 128);
-    int per = (nch == 1 ? 640 : 512) / nt;
-    if (per > 8) per = 8;
-    if (per < 1) per = 1;
-    const int64_t b = (int64_t)num_sms * per;
+int residual_norm_bwd_blocks(int64_t M, int64_t K, bool ckpt, int num_sms) {
+    const int64_t b = (int64_t)num_sms * bwd_shape(K, ckpt).per_sm;
     return (int)(M < b ? M : b);
 }
 
 template <bool POST, bool GATE, bool CK>
 static cudaError_t launch_bwd_t(const fp8rl_residual_norm_bwd_args& a, int64_t M, int64_t K, float* ws, int nb,
                                 cudaStream_t st) {
-    const int nch = bwd_nch(K);
-    const int nt = norm_threads((K / nch + 127) / 128 * 128);
-    if (nch == 1) k_residual_norm_bwd<POST, GATE, CK, 1><<<nb, nt, 0, st>>>(a, M, K, ws);
-    else k_residual_norm_bwd<POST, GATE, CK, 2><<<nb, nt, 0, st>>>(a, M, K, ws);
+    const BwdShape s = bwd_shape(K, CK);
+    auto kern = s.nch == 1 ? k_residual_norm_bwd<POST, GATE, CK, 1> : k_residual_norm_bwd<POST, GATE, CK, 2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    if (e != cudaSuccess) return e;
+    kern<<<nb, s.nt, s.smem, st>>>(a, M, K, s.slots, ws);
     return cudaGetLastError();
 }
 
@@ -415,10 +506,16 @@ cudaError_t launch_residual_norm_bwd(const fp8rl_residual_norm_bwd_args& a, int6
         else e = ck ? launch_bwd_t<false, false, true>(a, M, K, ws, nblocks, st) : launch_bwd_t<false, false, false>(a, M, K, ws, nblocks, st);
     }
     if (e != cudaSuccess) return e;
-    k_resnorm_colsum<<<dim3((unsigned)(K / 32), 3, 1), 256, 0, st>>>(ws, nblocks, K, a.dpre,
-                                                                    a.post_gamma ? a.dpost : nullptr,
-                                                                    a.gate ? a.dgate : nullptr);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(K / 32), a.post_gamma || a.gate ? 2u : 1u, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_resnorm_colsum, a, (const float*)ws, nblocks, K);
 }
 
 }  // namespace fp8rl
