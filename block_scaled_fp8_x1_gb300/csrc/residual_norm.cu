@@ -201,12 +201,12 @@ cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, i
 namespace {
 
 // One row's words of a thread's chunk of 8 columns, as they lie in its slot of shared memory:
-// dz and dh (BF16), then h' and y (BF16, or E4M3 codes and their group's scale).  A thread copies
+// dz and dh (BF16), then h' and y (BF16, or E4M3 codes).  A thread copies
 // and reads only its own chunks, so the copies need no barrier, only its own wait.
 template <bool CK>
 struct Slot {
     static constexpr int SAVED = CK ? 8 : 16;
-    static constexpr int BYTES = 32 + 2 * SAVED + (CK ? 8 : 0);   // a chunk of one thread
+    static constexpr int BYTES = 32 + 2 * SAVED;   // a chunk of one thread
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
@@ -225,11 +225,6 @@ __device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
 
 // Two E4M3 codes to FP32, exactly: through FP16, which holds every finite E4M3.
 __device__ __forceinline__ float2 e4m3_pair(uint32_t codes) {
@@ -244,12 +239,12 @@ __device__ __forceinline__ float2 e4m3_pair(uint32_t codes) {
     return d;
 }
 
-// Eight saved values times f (and times the checkpoint's scale).
+// Eight saved values times f (a checkpoint's scale is in f).
 template <bool CK>
-__device__ __forceinline__ void saved_times(uint32_t words, uint32_t scale, float f, float2 (&x)[4]) {
+__device__ __forceinline__ void saved_times(uint32_t words, float f, float2 (&x)[4]) {
     if (CK) {
         const uint2 c = lds_v2(words);
-        const float2 k = both(lds_f32(scale) * f);
+        const float2 k = both(f);
         #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(e4m3_pair((j < 2 ? c.x : c.y) >> (16 * (j & 1))), k);
     } else {
@@ -282,14 +277,13 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
     const int64_t m1 = m0 + rows < M ? m0 + rows : M;
     const float inv_k = __fdiv_rn(1.0f, (float)K);
     int par = 0;
-    // slot layout: for each chunk index i, arrays over the threads of dz, dh, h', y (and scales)
+    // slot layout: for each chunk index i, arrays over the threads of dz, dh, h', y
     const uint32_t base = smem_u32(rn_smem);
     const uint32_t chunk = (uint32_t)nt * SL::BYTES, slot_bytes = chunk * NCH;
-    auto at = [&](int slot, int i, int what) -> uint32_t {   // 0 dz, 1 dh, 2 h', 3 y, 4 sh, 5 sy
+    auto at = [&](int slot, int i, int what) -> uint32_t {   // 0 dz, 1 dh, 2 h', 3 y
         const uint32_t b = base + (uint32_t)slot * slot_bytes + (uint32_t)i * chunk;
         if (what < 2) return b + (uint32_t)(what * nt + tid) * 16u;
-        if (what < 4) return b + (uint32_t)nt * 32u + (uint32_t)((what - 2) * nt + tid) * SL::SAVED;
-        return b + (uint32_t)nt * (32u + 2u * SL::SAVED) + (uint32_t)((what - 4) * nt + tid) * 4u;
+        return b + (uint32_t)nt * 32u + (uint32_t)((what - 2) * nt + tid) * SL::SAVED;
     };
     auto copy_row = [&](int64_t m, int slot) {
         if (m < m1) {
@@ -301,11 +295,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
                 if (a.dh) cp_async_16(at(slot, i, 1), a.dh + m * a.lddh + c);
                 if (CK) {
                     cp_async_8(at(slot, i, 2), a.qh + m * K + c);
-                    cp_async_4(at(slot, i, 4), a.sh + (c >> 7) * M + m, 4);
-                    if (NEED_Y) {
-                        cp_async_8(at(slot, i, 3), a.qy + m * K + c);
-                        cp_async_4(at(slot, i, 5), a.sy + (c >> 7) * M + m, 4);
-                    }
+                    if (NEED_Y) cp_async_8(at(slot, i, 3), a.qy + m * K + c);
                 } else {
                     cp_async_16(at(slot, i, 2), a.h + m * a.ldh + c);
                     if (NEED_Y) cp_async_16(at(slot, i, 3), a.y + m * a.ldy + c);
@@ -326,10 +316,6 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
                 for (int w = 2; w < 4; ++w)
                     #pragma unroll
                     for (int o = 0; o < SL::SAVED; o += 4) st_shared_b32(at(sl, i, w) + o, 0);
-                if (CK) {
-                    st_shared_b32(at(sl, i, 4), 0);
-                    st_shared_b32(at(sl, i, 5), 0);
-                }
             }
         }
     for (int sl = 0; sl < slots - 1; ++sl) copy_row(m0 + sl, sl);
@@ -349,22 +335,42 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
             a_pre[i][j] = a_v[i][j] = both(0.0f);
         }
     }
-    float r_next = m0 < m1 ? a.r_pre[m0] : 0.0f, ry_next = POST && m0 < m1 ? a.r_post[m0] : 1.0f;
+    // the next row's statistics and the checkpoints' scales, one row ahead in registers
+    float r_next = 0.0f, ry_next = 1.0f, sh_next[NCH], sy_next[NCH];
+    auto load_scales = [&](int64_t m) {
+        if (m >= m1) return;
+        r_next = a.r_pre[m];
+        if (POST) ry_next = a.r_post[m];
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int64_t c = 8 * (int64_t)(tid + nt * i);
+            if (CK && c < K) {
+                sh_next[i] = a.sh[(c >> 7) * M + m];
+                if (NEED_Y) sy_next[i] = a.sy[(c >> 7) * M + m];
+            }
+        }
+    };
+    #pragma unroll
+    for (int i = 0; i < NCH; ++i) sh_next[i] = sy_next[i] = CK ? 0.0f : 1.0f;
+    load_scales(m0);
     __syncthreads();   // s_sum is zero
     int slot = 0;
     for (int64_t m = m0; m < m1; ++m) {
         const float r = r_next, ry = ry_next;
-        if (m + 1 < m1) {
-            r_next = a.r_pre[m + 1];
-            if (POST) ry_next = a.r_post[m + 1];
+        float sh[NCH], sy[NCH];
+        #pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            sh[i] = sh_next[i] * r;
+            sy[i] = POST ? sy_next[i] * ry : sy_next[i];
         }
+        load_scales(m + 1);
         // this row's copies have landed when at most the slots - 2 later ones are in flight
         if (slots == 4) cp_async_wait_group<2>();
         else cp_async_wait_group<1>();
         float2 x[NCH][4], t[NCH][4], part = both(0.0f);
         #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            saved_times<CK>(at(slot, i, 2), at(slot, i, 4), r, x[i]);
+            saved_times<CK>(at(slot, i, 2), sh[i], x[i]);
             const uint4 dz = lds_v4(at(slot, i, 0));
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
         for (int i = 0; i < NCH; ++i) {
             const int64_t c = 8 * (int64_t)(tid + nt * i);
             const uint4 dh = lds_v4(at(slot, i, 1));
-            if (NEED_Y) saved_times<CK>(at(slot, i, 3), at(slot, i, 5), POST ? ry : 1.0f, y[i]);
+            if (NEED_Y) saved_times<CK>(at(slot, i, 3), sy[i], y[i]);
             uint32_t o[4];
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
