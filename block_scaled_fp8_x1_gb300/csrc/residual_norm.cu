@@ -57,53 +57,78 @@ __device__ __noinline__ uint2 encode8_slow(uint4 v, float s) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// 1x128 codes of a row: thread t holds 8 columns of BF16 pairs, so a group is 16 lanes.  Every
-// lane of the warp takes part.
-__device__ __forceinline__ void quant_row(const uint4& v, bool act, uint8_t* q, float* s) {
-    uint32_t mx = absmax2(absmax2(absmax2(absmax2(0u, v.x), v.y), v.z), v.w);
-    mx = max(mx & 0xFFFFu, mx >> 16);
+// Largest |BF16| of eight values, per half of the word.
+__device__ __forceinline__ uint32_t max8(const uint4& v) { return absmax2(absmax2(absmax2(absmax2(0u, v.x), v.y), v.z), v.w); }
+
+// 1x128 codes of G groups of 128 that a half-warp holds, 8 values a lane and group.  The maxima
+// are reduced two to a word; lane g of the half-warp forms the scale of group g, once, stores it
+// at sp (null: a group that is not written), and hands it to the others.  Every lane of the warp
+// takes part; `codes` gets the eight codes of each group.
+template <int G>
+__device__ __forceinline__ void quant_groups(const uint4 (&v)[G], float* sp, uint2 (&codes)[G]) {
+    const int lane = threadIdx.x & 31, me = lane & 15;
+    uint32_t mx[(G + 1) / 2];
     #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (!act) return;
-    const FastScale f = fast_scale(bf16_bits_amax_to_f32(mx));
-    uint2 c = make_uint2(flip_codes(encode_pair_neg(pair(v.x), f.s, f.nr), encode_pair_neg(pair(v.y), f.s, f.nr), f.keep),
-                         flip_codes(encode_pair_neg(pair(v.z), f.s, f.nr), encode_pair_neg(pair(v.w), f.s, f.nr), f.keep));
-    if (f.slow) c = encode8_slow(v, f.s);
-    *reinterpret_cast<uint2*>(q) = c;
-    if ((threadIdx.x & 15) == 0) *s = f.s;
+    for (int g = 0; g < G; g += 2) {
+        const uint32_t w0 = max8(v[g]), w1 = g + 1 < G ? max8(v[g + 1 < G ? g + 1 : g]) : 0u;
+        uint32_t m = __vmaxu2(__byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632));
+        #pragma unroll
+        for (int off = 8; off >= 1; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+        mx[g / 2] = m;
+    }
+    uint32_t mine = mx[0];
+    #pragma unroll
+    for (int i = 1; i < (G + 1) / 2; ++i) mine = (me >> 1) == i ? mx[i] : mine;
+    const FastScale f = fast_scale(bf16_bits_amax_to_f32((me & 1) ? mine >> 16 : mine & 0xFFFFu));
+    if (sp) *sp = f.s;
+    const bool slow = __any_sync(0xffffffffu, me < G && f.slow);
+    #pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float sg = __shfl_sync(0xffffffffu, f.s, (lane & 16) | g), nr = __shfl_sync(0xffffffffu, f.nr, (lane & 16) | g);
+        const uint32_t keep = sg == 0.0f ? 0u : 0xFFFFFFFFu;
+        codes[g] = make_uint2(flip_codes(encode_pair_neg(pair(v[g].x), sg, nr), encode_pair_neg(pair(v[g].y), sg, nr), keep),
+                              flip_codes(encode_pair_neg(pair(v[g].z), sg, nr), encode_pair_neg(pair(v[g].w), sg, nr), keep));
+        if (slow && sg > 0.0f && scale_is_slow(sg)) codes[g] = encode8_slow(v[g], sg);
+    }
 }
 
-__device__ __forceinline__ float rstd_of(float sumsq, float k, float eps) {
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, k), eps)));
-}
+// 1/sqrt(mean + eps) by the hardware's reciprocal square root (2 ulp).
+__device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) { return rsqrtf(fmaf(sumsq, inv_k, eps)); }
 
 }  // namespace
 
 // One row per CTA at a time; thread t holds columns 8 (t + NT i), i < NCH.  The next row's words
 // are requested before this row is reduced.  The layout depends on K alone, so a token's row has
-// the same bits alone and in a batch.
-template <bool POST, int NCH>
+// the same bits alone and in a batch.  Q: z is quantized; CK: h' or y or both are.
+template <bool POST, bool Q, bool CK, int NCH>
 __global__ void __launch_bounds__(512, 2) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
-    extern __shared__ __align__(16) float s_w[];      // alpha * gate * g_post [K]
+    extern __shared__ __align__(16) float2 s_w[];     // alpha * gate * g_post, [NCH][4 pairs][threads]
     __shared__ float s_sum[2][32];
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const float kf = (float)K;
+    const int tid = threadIdx.x, nt = blockDim.x, me = tid & 15;
+    const float inv_k = __fdiv_rn(1.0f, (float)K);
     int par = 0;
     uint4 pre[NCH];
     #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int c = 8 * (tid + nt * i);
-        const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-        pre[i] = make_uint4(0, 0, 0, 0);
-        if (c < K) {
-            const uint4 g = a.gate ? ld_v4(a.gate + c) : one;
-            const uint4 p = POST ? ld_v4(a.post_gamma + c) : one;
-            pre[i] = ld_v4(a.pre_gamma + c);
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) s_w[c + j] = a.alpha * elem(g, j) * elem(p, j);
-        }
+        const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), zero = make_uint4(0, 0, 0, 0);
+        const uint4 g = c < K ? (a.gate ? ld_v4(a.gate + c) : one) : zero;
+        const uint4 p = c < K && POST ? ld_v4(a.post_gamma + c) : one;
+        pre[i] = c < K ? ld_v4(a.pre_gamma + c) : zero;
+        #pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s_w[(i * 4 + j) * nt + tid] = __fmul2_rn(__fmul2_rn(both(a.alpha), pair(word(g, j))), pair(word(p, j)));
     }
     if (tid < 32) s_sum[0][tid] = s_sum[1][tid] = 0.0f;
+    // groups of a half-warp: z's chunks, then h's, then y's; lane `me` stores the scale of group me
+    constexpr int G = NCH * ((Q ? 1 : 0) + (CK ? 2 : 0));
+    float* sp = nullptr;
+    if (me < G) {
+        const int which = me / NCH + (Q ? 0 : 1);
+        const int64_t c = 8 * (int64_t)((tid & ~15) + nt * (me % NCH));
+        float* s = which == 0 ? a.s : which == 1 ? a.sh : a.sy;
+        if (s && c < K) sp = s + (c >> 7) * M;
+    }
     __syncthreads();
     uint4 nh[NCH], ny[NCH];
     auto load_row = [&](int64_t m) {
@@ -133,67 +158,82 @@ __global__ void __launch_bounds__(512, 2) k_residual_norm(const fp8rl_residual_n
             for (int i = 0; i < NCH; ++i)
                 #pragma unroll
                 for (int j = 0; j < 4; ++j) ss = __ffma2_rn(pair(word(yv[i], j)), pair(word(yv[i], j)), ss);
-            ry = rstd_of(block_sum(ss.x + ss.y, s_sum[par]), kf, a.eps);
+            ry = rstd_of(block_sum(ss.x + ss.y, s_sum[par]), inv_k, a.eps);
             par ^= 1;
         }
         float2 ss = both(0.0f);
         #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = 8 * (tid + nt * i);
             uint32_t o[4];
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 w = c < K ? *reinterpret_cast<const float2*>(s_w + c + 2 * j) : both(0.0f);
-                const float2 x = __ffma2_rn(__fmul2_rn(pair(word(yv[i], j)), both(ry)), w, pair(word(hv[i], j)));
+                const float2 x = __ffma2_rn(__fmul2_rn(pair(word(yv[i], j)), both(ry)), s_w[(i * 4 + j) * nt + tid], pair(word(hv[i], j)));
                 o[j] = pack_bf16x2(x.x, x.y);
                 ss = __ffma2_rn(pair(o[j]), pair(o[j]), ss);
             }
             hv[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        const float r = rstd_of(block_sum(ss.x + ss.y, s_sum[par]), kf, a.eps);
+        const float r = rstd_of(block_sum(ss.x + ss.y, s_sum[par]), inv_k, a.eps);
         par ^= 1;
         if (tid == 0) {
             a.r_pre[m] = r;
             if (POST) a.r_post[m] = ry;
         }
+        uint4 z[NCH];
         #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int c = 8 * (tid + nt * i);
-            const bool act = c < K;
             uint32_t o[4];
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 x = __fmul2_rn(__fmul2_rn(pair(word(hv[i], j)), both(r)), pair(word(pre[i], j)));
                 o[j] = pack_bf16x2(x.x, x.y);
             }
-            const uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
-            if (act) *reinterpret_cast<uint4*>(a.h_out + m * K + c) = hv[i];
-            const int64_t sc = (int64_t)(c >> 7) * M + m;
-            if (a.z && act) *reinterpret_cast<uint4*>(a.z + m * K + c) = z;
-            if (a.q) quant_row(z, act, a.q + m * K + c, a.s + sc);
-            if (a.qh) quant_row(hv[i], act, a.qh + m * K + c, a.sh + sc);
-            if (a.qy) quant_row(yv[i], act, a.qy + m * K + c, a.sy + sc);
+            z[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c < K) {
+                *reinterpret_cast<uint4*>(a.h_out + m * K + c) = hv[i];
+                if (a.z) *reinterpret_cast<uint4*>(a.z + m * K + c) = z[i];
+            }
+        }
+        if constexpr (G > 0) {
+            uint4 v[G];
+            uint2 codes[G];
+            #pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int which = g / NCH + (Q ? 0 : 1), i = g % NCH;
+                v[g] = which == 0 ? z[i] : which == 1 ? hv[i] : yv[i];
+            }
+            quant_groups<G>(v, sp ? sp + m : nullptr, codes);
+            #pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int which = g / NCH + (Q ? 0 : 1), c = 8 * (tid + nt * (g % NCH));
+                uint8_t* q = which == 0 ? a.q : which == 1 ? a.qh : a.qy;
+                if (c < K && (which == 0 || q)) *reinterpret_cast<uint2*>(q + m * K + c) = codes[g];
+            }
         }
     }
 }
 
 static int norm_threads(int64_t K) { return (int)((K / 8 + 31) / 32 * 32); }
 
-template <int NCH>
+template <bool POST, int NCH>
 static cudaError_t launch_fwd_t(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
     const int nt = norm_threads((K / 8 + NCH - 1) / NCH * 8);
-    auto kern = a.post_gamma ? k_residual_norm<true, NCH> : k_residual_norm<false, NCH>;
+    const bool ck = a.qh || a.qy;
+    auto kern = a.q ? (ck ? k_residual_norm<POST, true, true, NCH> : k_residual_norm<POST, true, false, NCH>)
+                    : (ck ? k_residual_norm<POST, false, true, NCH> : k_residual_norm<POST, false, false, NCH>);
+    const size_t smem = (size_t)nt * NCH * 32;
     int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, (size_t)K * 4);
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
-    kern<<<(unsigned)(M < grid ? M : grid), nt, (size_t)K * 4, st>>>(a, M, K);
+    kern<<<(unsigned)(M < grid ? M : grid), nt, smem, st>>>(a, M, K);
     return cudaGetLastError();
 }
 
 cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
-    if (K <= 4096) return launch_fwd_t<1>(a, M, K, num_sms, st);
-    return launch_fwd_t<2>(a, M, K, num_sms, st);
+    if (K <= 4096) return a.post_gamma ? launch_fwd_t<true, 1>(a, M, K, num_sms, st) : launch_fwd_t<false, 1>(a, M, K, num_sms, st);
+    return a.post_gamma ? launch_fwd_t<true, 2>(a, M, K, num_sms, st) : launch_fwd_t<false, 2>(a, M, K, num_sms, st);
 }
 
 // ------------------------------------------------------------------------------------ backward
