@@ -133,6 +133,16 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
     return F2{s, e};
 }
 
+// 1 / (1 + exp(-g)) by the hardware's exp2 and reciprocal in their flushing forms: the same bits
+// as __fdividef(1, 1 + __expf(-g)), without that form's range scaling (what it would save is
+// added to 1, or is a sigmoid below 2^-126, zero either way).
+__device__ __forceinline__ float sigmoid_fast(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
 // One thread's 8 rows x 8 columns of the staged tile -> BF16 words of y (the value that is
 // quantized): x itself, bf16((x*rstd)*gamma), or bf16(silu(g)*u).  The stage holds the
 // 128x128 BF16 tile row-major (256 bytes per row); SiLU-mul stages the up tile after it.
@@ -185,6 +195,16 @@ __device__ __forceinline__ void rows_from_smem(const uint8_t* stage, const Panel
             for (int j = 0; j < 4; ++j) {
                 const float2 y = __fmul2_rn(__fmul2_rn(make_float2(bf16_lo(xv[j]), bf16_hi(xv[j])), make_float2(r, r)), gam[j]);
                 w[i][j] = pack_bf16x2(y.x, y.y);
+            }
+        } else if (PRO == PRO_SILU_CK) {  // SILU's values on packed pairs
+            const uint4 u = *reinterpret_cast<const uint4*>(stage + 128 * 256 + (R0 + i) * 256 + C0 * 2);
+            const uint32_t uv[4] = {u.x, u.y, u.z, u.w};
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 g = make_float2(bf16_lo(xv[j]), bf16_hi(xv[j]));
+                const float2 h = __fmul2_rn(__fmul2_rn(g, make_float2(sigmoid_fast(g.x), sigmoid_fast(g.y))),
+                                            make_float2(bf16_lo(uv[j]), bf16_hi(uv[j])));
+                w[i][j] = pack_bf16x2(h.x, h.y);
             }
         } else {  // SILU: h = bf16(silu(g) * u), silu(g) = g / (1 + exp(-g))
             const uint4 u = *reinterpret_cast<const uint4*>(stage + 128 * 256 + (R0 + i) * 256 + C0 * 2);
@@ -269,17 +289,14 @@ __device__ __forceinline__ void silu_bwd_ckpt_from_smem(uint8_t* stage, int R0, 
         for (int j = 0; j < 4; ++j) {
             const float2 g2 = __fmul2_rn(e4m3_pair((j < 2 ? gc.x : gc.y) >> (16 * (j & 1))), make_float2(sg_, sg_));
             const float2 u2 = __fmul2_rn(e4m3_pair((j < 2 ? uc.x : uc.y) >> (16 * (j & 1))), make_float2(su_, su_));
-            float og[2], ou[2];
-            #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float g = e ? g2.y : g2.x, uu = e ? u2.y : u2.x;
-                const float dd = e ? bf16_hi(dv[j]) : bf16_lo(dv[j]);
-                const float sg = __fdividef(1.0f, 1.0f + __expf(-g));
-                og[e] = __fmul_rn(__fmul_rn(__fmul_rn(dd, uu), sg), __fmaf_rn(g, __fsub_rn(1.0f, sg), 1.0f));
-                ou[e] = __fmul_rn(dd, __fmul_rn(g, sg));
-            }
-            w[i][j] = pack_bf16x2(og[0], og[1]);
-            du[j] = pack_bf16x2(ou[0], ou[1]);
+            const float2 d2 = make_float2(bf16_lo(dv[j]), bf16_hi(dv[j]));
+            const float2 sg = make_float2(sigmoid_fast(g2.x), sigmoid_fast(g2.y));
+            const float2 one = make_float2(1.0f, 1.0f);
+            const float2 c = __ffma2_rn(sg, make_float2(-1.0f, -1.0f), one);
+            const float2 og = __fmul2_rn(__fmul2_rn(__fmul2_rn(d2, u2), sg), __ffma2_rn(g2, c, one));
+            const float2 ou = __fmul2_rn(d2, __fmul2_rn(g2, sg));
+            w[i][j] = pack_bf16x2(og.x, og.y);
+            du[j] = pack_bf16x2(ou.x, ou.y);
         }
         *dp = make_uint4(du[0], du[1], du[2], du[3]);
     }
@@ -311,14 +328,24 @@ __device__ __noinline__ uint4 encode4_slow(float2 x0, float2 x1, float2 x2, floa
 __device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_t* q, float* s, int64_t ldq, int64_t M,
                                                int64_t r0, int64_t tt, int C0, int lane) {
     const int cl = lane & 15;
-    uint32_t mine = 0;   // maximum of row r0 + (cl & 7)
+    uint32_t pm[4];   // maxima of rows (2k, 2k + 1), a half each
     #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t v = absmax2(absmax2(absmax2(absmax2(0u, w[i][0]), w[i][1]), w[i][2]), w[i][3]);
+    for (int k = 0; k < 4; ++k) {
+        uint32_t m2[2];
         #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
-        if ((cl & 7) == i) mine = max(v & 0xFFFFu, v >> 16);
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t(&v)[4] = w[2 * k + e];
+            m2[e] = absmax2(absmax2(absmax2(absmax2(0u, v[0]), v[1]), v[2]), v[3]);
+        }
+        pm[k] = __vmaxu2(__byte_perm(m2[0], m2[1], 0x5410), __byte_perm(m2[0], m2[1], 0x7632));
     }
+    #pragma unroll
+    for (int off = 8; off >= 1; off >>= 1)
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) pm[k] = __vmaxu2(pm[k], __shfl_xor_sync(0xffffffffu, pm[k], off));
+    const int ri = cl & 7;   // this lane forms the scale of row r0 + ri
+    const uint32_t pw = (ri >> 1) == 0 ? pm[0] : (ri >> 1) == 1 ? pm[1] : (ri >> 1) == 2 ? pm[2] : pm[3];
+    const uint32_t mine = (ri & 1) ? (pw >> 16) : (pw & 0xFFFFu);
     const FastScale fs = fast_scale(bf16_bits_amax_to_f32(mine));
     if (cl < 8 && r0 + cl < M) s[tt * M + r0 + cl] = fs.s;
     #pragma unroll
@@ -837,7 +864,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
                 rows_from_smem<PRO_COPY>(stage + half_gu * 128 * 256, a, 0, R0, C0, nullptr, rg0, w);
                 quant_rows_8x8(w, a.qc, a.sc, 2 * a.K, a.M, m0 + R0, half_gu * ntiles + t, C0, lane);
             }
-            rows_from_smem<PRO_SILU>(stage, a, t * 128, R0, C0, nullptr, rg0, w);
+            rows_from_smem<PRO_SILU_CK>(stage, a, t * 128, R0, C0, nullptr, rg0, w);
             quantize_tile(w, t, smem_u32(stages + PS::COLQ_OFF) + (uint32_t)(item & 1) * (128u * 128u), 1);
         } else {
             float rg[8];

@@ -100,8 +100,8 @@ __device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) { 
 // One row per CTA at a time; thread t holds columns 8 (t + NT i), i < NCH.  The next row's words
 // are requested before this row is reduced.  The layout depends on K alone, so a token's row has
 // the same bits alone and in a batch.  Q: z is quantized; CK: h' or y or both are.
-template <bool POST, bool Q, bool CK, int NCH>
-__global__ void __launch_bounds__(512, 2) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
+template <bool POST, bool Q, bool CK, int NCH, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
     extern __shared__ __align__(16) float2 s_w[];     // alpha * gate * g_post, [NCH][4 pairs][threads]
     __shared__ float s_sum[2][32];
     const int tid = threadIdx.x, nt = blockDim.x, me = tid & 15;
@@ -216,12 +216,12 @@ __global__ void __launch_bounds__(512, 2) k_residual_norm(const fp8rl_residual_n
 
 static int norm_threads(int64_t K) { return (int)((K / 8 + 31) / 32 * 32); }
 
-template <bool POST, int NCH>
+template <bool POST, int NCH, int MAXT, int MINB>
 static cudaError_t launch_fwd_t(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
     const int nt = norm_threads((K / 8 + NCH - 1) / NCH * 8);
     const bool ck = a.qh || a.qy;
-    auto kern = a.q ? (ck ? k_residual_norm<POST, true, true, NCH> : k_residual_norm<POST, true, false, NCH>)
-                    : (ck ? k_residual_norm<POST, false, true, NCH> : k_residual_norm<POST, false, false, NCH>);
+    auto kern = a.q ? (ck ? k_residual_norm<POST, true, true, NCH, MAXT, MINB> : k_residual_norm<POST, true, false, NCH, MAXT, MINB>)
+                    : (ck ? k_residual_norm<POST, false, true, NCH, MAXT, MINB> : k_residual_norm<POST, false, false, NCH, MAXT, MINB>);
     const size_t smem = (size_t)nt * NCH * 32;
     int per_sm = 0;
     cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, smem);
@@ -231,9 +231,21 @@ static cudaError_t launch_fwd_t(const fp8rl_residual_norm_args& a, int64_t M, in
     return cudaGetLastError();
 }
 
+template <int NCH, int MAXT, int MINB>
+static cudaError_t launch_fwd(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
+    return a.post_gamma ? launch_fwd_t<true, NCH, MAXT, MINB>(a, M, K, num_sms, st)
+                        : launch_fwd_t<false, NCH, MAXT, MINB>(a, M, K, num_sms, st);
+}
+
 cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
-    if (K <= 4096) return a.post_gamma ? launch_fwd_t<true, 1>(a, M, K, num_sms, st) : launch_fwd_t<false, 1>(a, M, K, num_sms, st);
-    return a.post_gamma ? launch_fwd_t<true, 2>(a, M, K, num_sms, st) : launch_fwd_t<false, 2>(a, M, K, num_sms, st);
+    // Two chunks of 8 columns a thread, as many CTAs on an SM as registers allow without spills
+    // (the compiler's bound is for the widest row of each range).  16384 x 5120, BF16 out /
+    // quantized with both checkpoints, in us: 103 / 149 so, 117 / 166 with three CTAs at 64
+    // registers, 102 / 202 with one chunk and 640 threads, 114 / 172 with four chunks.
+    if (K <= 2560) return launch_fwd<2, 160, 4>(a, M, K, num_sms, st);
+    if (K <= 4096) return launch_fwd<2, 256, 3>(a, M, K, num_sms, st);
+    if (K <= 5120) return launch_fwd<2, 320, 2>(a, M, K, num_sms, st);
+    return launch_fwd<2, 512, 1>(a, M, K, num_sms, st);
 }
 
 // ------------------------------------------------------------------------------------ backward
