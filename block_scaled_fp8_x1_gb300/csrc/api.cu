@@ -1027,9 +1027,8 @@ static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_r
     for (int s = 1; s <= 8; ++s) {
         if (splits_req > 0 && s != splits_req) continue;
         if (s > nkb || matvec_smem(M, (int)nkb, s) > kMatvecMaxSmem) continue;
-        for (int w = 1; w <= 8; w *= 2) {
-            const int per_sm = M <= 8 && matvec_smem(M, (int)nkb, s) <= kMatvecMaxSmem / 2 ? 2 : 1;
-            const int64_t groups = (tiles + 8 / w - 1) / (8 / w), at_once = (int64_t)sms * per_sm / s;
+        for (int w = 1; w <= kMatvecWarps; w *= 2) {
+            const int64_t per = kMatvecWarps / w, groups = (tiles + per - 1) / per, at_once = sms / s;
             const int64_t rounds = (groups + at_once - 1) / at_once;
             const int64_t units = ((nkb + s - 1) / s + w - 1) / w;
             const double cost = (double)rounds * ((double)units + (s > 1 ? 1.5 : 0.5));
@@ -1043,9 +1042,8 @@ static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_r
     *splits = best_s;
     *wk = best_w;
     if (best_s == 0) return;
-    const int per_sm = M <= 8 && matvec_smem(M, (int)nkb, best_s) <= kMatvecMaxSmem / 2 ? 2 : 1;
-    const int64_t groups = (tiles + 8 / best_w - 1) / (8 / best_w);
-    *clusters = (int)std::min<int64_t>(groups, best_s > 1 ? groups : (int64_t)sms * per_sm);
+    const int64_t per = kMatvecWarps / best_w, groups = (tiles + per - 1) / per;
+    *clusters = (int)std::min<int64_t>(groups, best_s > 1 ? groups : (int64_t)sms);
 }
 
 fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,

@@ -36,7 +36,7 @@ struct MatvecParams {
     int nkb;                 // K / 128 (even)
     int tiles;               // N / 32 (a multiple of 4)
     int splits;              // CTAs of a cluster that share K, 1..8
-    int wk;                  // warps of a CTA that share K: 1, 2, 4 or 8
+    int wk;                  // warps of a CTA that share K: 1, 2, 4, 8 or 16
     const uint16_t* x;
     int64_t ldx;
     const uint8_t* qw;
@@ -46,9 +46,11 @@ struct MatvecParams {
     int64_t ldy;
 };
 constexpr int kMatvecMaxTokens = 16;
+constexpr int kMatvecWarps = 16;
 constexpr size_t kMatvecMaxSmem = 224 * 1024;
 size_t matvec_smem(int M, int nkb, int splits);   // dynamic shared memory of a CTA
-// `clusters` of p.splits CTAs, each taking every clusters-th group of 8 / wk tiles of 32 rows.
+// `clusters` of p.splits CTAs, each taking every clusters-th group of kMatvecWarps / wk tiles of
+// 32 rows.
 cudaError_t launch_matvec_nvfp4(const MatvecParams& p, int clusters, cudaStream_t st);
 
 }  // namespace fp8rl
