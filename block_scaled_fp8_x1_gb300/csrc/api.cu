@@ -1020,7 +1020,12 @@ fp8rl_status fp8rl_gemm_nvfp4(const uint8_t* qx, const uint8_t* sfx, const float
 }
 
 // How a product of M tokens with an [N][K] weight shares K: the cluster size and the warps of a
-// CTA (matvec.cu).
+// CTA (matvec.cu), by the time of the busiest warp in units of 32 rows x 128 of K: its units, plus
+// per round of tiles 1.2 for the CTA's own reduction or 1.8 + 0.15 S for a cluster's, plus 0.2 for each
+// pair of a token's blocks that its warp lays out.  Fitted on the 7B linears and 14336 x 4096, one
+// to 16 tokens, every split timed: the choice is within 4% of the fastest there (3584 x 3584 at 16
+// tokens: 9.5 us in clusters of 5, 12.0 us without; 14336 x 4096 at one: 10.7 us in one round of
+// four warps a tile, 12.1 us in three rounds of 16).
 static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_req, int* splits, int* wk, int* clusters) {
     int best_s = 0, best_w = 1;
     double best = 1e30;
@@ -1031,7 +1036,8 @@ static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_r
             const int64_t per = kMatvecWarps / w, groups = (tiles + per - 1) / per, at_once = sms / s;
             const int64_t rounds = (groups + at_once - 1) / at_once;
             const int64_t units = ((nkb + s - 1) / s + w - 1) / w;
-            const double cost = (double)rounds * ((double)units + (s > 1 ? 1.5 : 0.5));
+            const double lay = (double)((M * ((nkb + s - 1) / s) + 2 * kMatvecWarps - 1) / (2 * kMatvecWarps));
+            const double cost = (double)rounds * ((double)units + (s > 1 ? 1.8 + 0.15 * s : 1.2)) + 0.2 * lay;
             if (cost < best - 1e-9) {
                 best = cost;
                 best_s = s;
