@@ -128,6 +128,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded libfp8rl (declared signatures); raises if it was never built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -102,6 +102,7 @@ __device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) { 
 // the same bits alone and in a batch.  Q: z is quantized; CK: h' or y or both are.
 template <bool POST, bool Q, bool CK, int NCH, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
+    grid_dependency_begin();
     extern __shared__ __align__(16) float2 s_w[];     // alpha * gate * g_post, [NCH][4 pairs][threads]
     __shared__ float s_sum[2][32];
     const int tid = threadIdx.x, nt = blockDim.x, me = tid & 15;
@@ -227,8 +228,7 @@ static cudaError_t launch_fwd_t(const fp8rl_residual_norm_args& a, int64_t M, in
     cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, nt, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
-    kern<<<(unsigned)(M < grid ? M : grid), nt, smem, st>>>(a, M, K);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3((unsigned)(M < grid ? M : grid)), dim3(nt), smem, st, a, M, K);
 }
 
 template <int NCH, int MAXT, int MINB>
@@ -318,6 +318,7 @@ __device__ __forceinline__ void saved_times(uint32_t words, float f, float2 (&x)
 template <bool POST, bool GATE, bool CK, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
     k_residual_norm_bwd(const fp8rl_residual_norm_bwd_args a, int64_t M, int64_t K, int slots, float* __restrict__ ws) {
+    grid_dependency_begin();
     constexpr bool NEED_Y = POST || GATE;
     using SL = Slot<CK>;
     extern __shared__ __align__(16) uint8_t rn_smem[];
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
 // block order, then the slices in order.
 __global__ void __launch_bounds__(256) k_resnorm_colsum(const fp8rl_residual_norm_bwd_args a, const float* __restrict__ ws,
                                                         int nblocks, int64_t K) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the rows are still worked on
+    grid_dependency_begin();   // launched while the rows are still worked on
     __shared__ float part[8][33];
     const int x = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t k = (int64_t)blockIdx.x * 32 + x;
@@ -548,8 +549,7 @@ static cudaError_t launch_bwd_t(const fp8rl_residual_norm_bwd_args& a, int64_t M
     auto kern = s.nch == 1 ? k_residual_norm_bwd<POST, GATE, CK, 1> : k_residual_norm_bwd<POST, GATE, CK, 2>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
     if (e != cudaSuccess) return e;
-    kern<<<nb, s.nt, s.smem, st>>>(a, M, K, s.slots, ws);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(nb), dim3(s.nt), s.smem, st, a, M, K, s.slots, ws);
 }
 
 cudaError_t launch_residual_norm_bwd(const fp8rl_residual_norm_bwd_args& a, int64_t M, int64_t K, float* ws,
@@ -564,16 +564,8 @@ cudaError_t launch_residual_norm_bwd(const fp8rl_residual_norm_bwd_args& a, int6
         else e = ck ? launch_bwd_t<false, false, true>(a, M, K, ws, nblocks, st) : launch_bwd_t<false, false, false>(a, M, K, ws, nblocks, st);
     }
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(K / 32), a.post_gamma || a.gate ? 2u : 1u, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_resnorm_colsum, a, (const float*)ws, nblocks, K);
+    return launch_dependent(k_resnorm_colsum, dim3((unsigned)(K / 32), a.post_gamma || a.gate ? 2u : 1u, 1), dim3(256), 0, st,
+                            a, (const float*)ws, nblocks, K);
 }
 
 }  // namespace fp8rl

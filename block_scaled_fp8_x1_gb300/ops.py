@@ -19,11 +19,13 @@ from ._abi import GemmOpts, check, lib
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle alone: the stream object that torch.cuda.current_stream builds costs 2 us
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _require(t: torch.Tensor, dtype: torch.dtype, name: str, device=None) -> None:
@@ -294,18 +296,19 @@ class ResidualNormGrads(NamedTuple):
 def _rows(t: torch.Tensor, name: str, shape, device) -> int:
     """Checks a bf16 matrix of contiguous rows and returns its row stride."""
     _require(t, torch.bfloat16, name, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _vector(t: Optional[torch.Tensor], name: str, dtype, n: int, device) -> None:
     if t is None:
         return
     _require(t, dtype, name, device)
-    if tuple(t.shape) != (n,):
+    if t.shape != (n,):
         raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(t.shape)}")
     _contig(t, name)
 
@@ -333,9 +336,9 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, pre_gamma: torch.Tensor, eps
     over a contiguous h."""
     _matrix(h, "h")
     _require(h, torch.bfloat16, "h")
-    M, K = h.shape
-    dev = h.device
-    ldh, ldy = _rows(h, "h", (M, K), dev), _rows(y, "y", (M, K), dev)
+    shape, dev = h.shape, h.device
+    M, K = shape
+    ldh, ldy = _rows(h, "h", shape, dev), _rows(y, "y", shape, dev)
     for t, n in ((pre_gamma, "pre_gamma"), (post_gamma, "post_gamma"), (gate, "gate")):
         _vector(t, n, torch.bfloat16, K, dev)
     if emit not in ("bf16", "fp8", "dual"):
@@ -374,7 +377,7 @@ def _saved(t, name: str, shape, dev):
     M, K = shape
     for c, n, dt, sh in ((q, f"{name} codes", torch.uint8, (M, K)), (s, f"{name} scales", torch.float32, (K // 128, M))):
         _require(c, dt, n, dev)
-        if tuple(c.shape) != sh:
+        if c.shape != sh:
             raise ValueError(f"{n}: expected shape {sh}, got {tuple(c.shape)}")
         _contig(c, n)
     return None, 0, _ptr(q), _ptr(s)
