@@ -639,15 +639,15 @@ def matvec_nvfp4(x: torch.Tensor, qw: torch.Tensor, sfw: torch.Tensor, gw: torch
     _require(x, torch.bfloat16, "x")
     M, K = x.shape
     dev = x.device
-    ldx = _rows(x, "x", (M, K), dev)
-    for t, n, dt in ((qw, "qw", torch.uint8), (sfw, "sfw", torch.uint8), (gw, "gw", torch.float32)):
-        _require(t, dt, n, dev)
-        _contig(t, n)
+    ldx = _rows(x, "x", x.shape, dev)
     N = gw.numel()
-    if tuple(qw.shape) != (N, K // 2) or K % 2 != 0:
+    _vector(gw, "gw", torch.float32, N, dev)
+    _require(qw, torch.uint8, "qw", dev)
+    _contig(qw, "qw")
+    if K % 2 != 0 or qw.shape != (N, K // 2):
         raise ValueError(f"qw: expected shape {(N, K // 2)}, got {tuple(qw.shape)}")
-    if N > 0 and sfw.numel() != nvfp4_scale_bytes(N, K):
-        raise ValueError(f"sfw: expected {nvfp4_scale_bytes(N, K)} bytes, got {sfw.numel()}")
+    # a 2 KB piece of scales per 128 rows x 256 of K; other K the library refuses
+    _vector(sfw, "sfw", torch.uint8, (N + 127) // 128 * (K // 256) * 2048 if K % 256 == 0 else sfw.numel(), dev)
     y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     ldy = _rows(y, "out", (M, N), dev)
     check(lib().fp8rl_matvec_nvfp4(_ptr(x), M, K, ldx, _ptr(qw), _ptr(sfw), _ptr(gw), N, _ptr(y), ldy,

@@ -104,3 +104,20 @@ def test_matvec_nvfp4_refusals(abi, kw, status):
     want = getattr(abi, "FP8RL_OK" if status == "OK" else f"FP8RL_ERR_{status}")
     assert abi.lib().fp8rl_matvec_nvfp4(a["x"], a["M"], a["K"], a["ldx"], a["q"], a["sf"], a["g"], a["N"], a["y"], a["ldy"],
                                         a["splits"], None) == want
+
+
+def test_binding_refuses_what_is_not_on_a_gpu_or_has_another_type():
+    """The binding's own checks answer before any CUDA call."""
+    import torch
+    from block_scaled_fp8_x1_gb300 import ops
+    b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    for call in (lambda x: ops.residual_norm(x, x, b(256), 1e-5), lambda x: ops.residual_norm_bwd(x, x, x, x, b(256), b(4)),
+                 lambda x: ops.silu_mul_quant_ckpt(x), lambda x: ops.matvec_nvfp4(x, x, x, x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(b(4, 256))
+        with pytest.raises(TypeError):
+            call(torch.zeros((4, 256)))
+        with pytest.raises(ValueError, match="matrix"):
+            call(b(256))
+    with pytest.raises(TypeError):
+        ops.silu_mul_bwd_quant_ckpt(b(4, 256), b(2, 4), b(4, 128))

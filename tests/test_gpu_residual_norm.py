@@ -257,3 +257,34 @@ def test_no_rows(fp8lib):
     assert g.dh.shape == (0, K)
     for v in (g.dpre, g.dpost, g.dgate):
         assert float(v.abs().max()) == 0.0
+
+
+def test_refusals(fp8lib):
+    M, K = 4, 256
+    h, y, pre, post, gate = inputs(M, K, True, True)
+    with pytest.raises(ValueError, match="y: expected shape"):
+        fp8lib.residual_norm(h, y[:3], pre, EPS)
+    with pytest.raises(ValueError, match="contiguous"):
+        fp8lib.residual_norm(h.t().contiguous().t(), y, pre, EPS)
+    with pytest.raises(ValueError, match="pre_gamma"):
+        fp8lib.residual_norm(h, y, pre[:128], EPS)
+    with pytest.raises(ValueError, match="emit"):
+        fp8lib.residual_norm(h, y, pre, EPS, emit="int8")
+    with pytest.raises(ValueError, match="on cpu|CUDA"):
+        fp8lib.residual_norm(h, y.cpu(), pre, EPS)
+    with pytest.raises(_abi.Fp8rlError) as e:
+        fp8lib.residual_norm(h, y, pre, EPS, emit="dual")          # M % 128
+    assert e.value.status == _abi.FP8RL_ERR_SHAPE
+    with pytest.raises(_abi.Fp8rlError) as e:
+        fp8lib.residual_norm(h[:, :200], y[:, :200], pre[:200], EPS)
+    assert e.value.status == _abi.FP8RL_ERR_SHAPE
+    f = fp8lib.residual_norm(h, y, pre, EPS, post_gamma=post, gate=gate, checkpoint=True)
+    dz = torch.zeros_like(h)
+    with pytest.raises(ValueError, match="r_post"):
+        fp8lib.residual_norm_bwd(dz, dz, f.h, y, pre, f.r_pre, post_gamma=post)
+    with pytest.raises(ValueError, match="y: needed"):
+        fp8lib.residual_norm_bwd(dz, dz, f.h, None, pre, f.r_pre, gate=gate)
+    with pytest.raises(ValueError, match="both"):
+        fp8lib.residual_norm_bwd(dz, dz, f.h_ckpt, y, pre, f.r_pre, gate=gate)
+    with pytest.raises(ValueError, match="h scales"):
+        fp8lib.residual_norm_bwd(dz, dz, (f.h_ckpt[0], f.h_ckpt[1].t()), None, pre, f.r_pre)
