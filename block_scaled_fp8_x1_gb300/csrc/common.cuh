@@ -346,10 +346,9 @@ __device__ __forceinline__ void cp_async_wait_group() {
 // ------------------------------------------------------------------------------ launches
 
 // First statement of a kernel launched by launch_dependent: the kernel's CTAs may be set up while
-// the stream's previous kernel ends, and touch no memory before that kernel's writes are visible;
-// a kernel launched the same way after this one may be set up in turn.
+// the stream's previous kernel ends, and touch no memory before that kernel's writes are visible.
 __device__ __forceinline__ void grid_dependency_begin() {
-    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 template <typename... P, typename... A>
 inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
