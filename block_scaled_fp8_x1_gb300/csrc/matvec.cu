@@ -81,6 +81,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same into a fresh sum.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 struct Unit {
     uint4 w[4];   // codes of rows 8o + g + 32 i, K = 32t .. 32t + 31
     uint4 sf;     // their scale atom row: word i = row i's four scales of 64 elements
@@ -183,13 +190,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
             }
             if (it0 + 2 * kWarps * XB < items + (tid >> 4)) load_x(it0 + 2 * kWarps * XB);
         }
-        // tokens past M: their columns are zero
-        if (!ONE)
-            for (int i = tid; i < kslice * TOK; i += kWarps * 32)
-                if (i % TOK >= p.M) inv[i] = 0.0f;
     }
     __syncthreads();
 
+    // this lane's column of each token group; columns past M repeat the last token and are not used
+    uint32_t x_lane[NT], x_swap[NT];
+    #pragma unroll
+    for (int a = 0; a < NT; ++a) {
+        const int m = 8 * a + g < p.M ? 8 * a + g : p.M - 1;
+        x_lane[a] = smem_u32(xs) + (uint32_t)(m * kXBlock);
+        x_swap[a] = 64u * (m & 1);
+    }
     int slot = 0;
     for (int tile0 = cl * per; tile0 < ntile; tile0 += ncl * per) {
         const int tile = tile0 + wt;
@@ -210,12 +221,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
                 asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sc[i]) : "h"(pr));
             }
             float acc[NT][2][4];
+            uint32_t s2[4][2];                               // !ONE: each group's scale in both halves
             #pragma unroll
-            for (int a = 0; a < NT; ++a)
-                #pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[a][b][c] = 0.0f;
+            for (int i = 0; i < 4; ++i) {
+                s2[i][0] = __byte_perm(sc[i], sc[i], 0x1010);
+                s2[i][1] = __byte_perm(sc[i], sc[i], 0x3232);
+            }
             #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 uint4 b[NT];
@@ -224,11 +235,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
                     b[0] = *reinterpret_cast<const uint4*>(at);
                 } else {
                     #pragma unroll
-                    for (int a = 0; a < NT; ++a) {
-                        b[a] = make_uint4(0, 0, 0, 0);
-                        const int m = 8 * a + g;
-                        if (m < p.M) b[a] = *reinterpret_cast<const uint4*>(xs + ((size_t)kb * p.M + m) * kXBlock + ((4 * jj + t) ^ (4 * (g & 1))) * 16);
-                    }
+                    for (int a = 0; a < NT; ++a)
+                        b[a] = lds_v4(x_lane[a] + (uint32_t)(kb * p.M * kXBlock) + (((uint32_t)(64 * jj + 16 * t)) ^ x_swap[a]));
                 }
                 #pragma unroll
                 for (int T = 0; T < 2; ++T) {
@@ -236,17 +244,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
                     e2m1x8(word(cur.w[2 * T], jj), ha);
                     e2m1x8(word(cur.w[2 * T + 1], jj), hb);
                     if (!ONE) {
-                        const uint32_t sa = __byte_perm(sc[2 * T], sc[2 * T], jj < 2 ? 0x1010 : 0x3232);
-                        const uint32_t sb = __byte_perm(sc[2 * T + 1], sc[2 * T + 1], jj < 2 ? 0x1010 : 0x3232);
                         #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            ha[i] = hmul2(ha[i], sa);
-                            hb[i] = hmul2(hb[i], sb);
+                            ha[i] = hmul2(ha[i], s2[2 * T][jj >> 1]);
+                            hb[i] = hmul2(hb[i], s2[2 * T + 1][jj >> 1]);
                         }
                     }
                     #pragma unroll
                     for (int a = 0; a < NT; ++a) {
-                        mma_f16(acc[a][T], ha[0], hb[0], ha[1], hb[1], b[a].x, b[a].y);
+                        if (jj == 0) mma_f16_first(acc[a][T], ha[0], hb[0], ha[1], hb[1], b[a].x, b[a].y);
+                        else mma_f16(acc[a][T], ha[0], hb[0], ha[1], hb[1], b[a].x, b[a].y);
                         mma_f16(acc[a][T], ha[2], hb[2], ha[3], hb[3], b[a].z, b[a].w);
                     }
                 }
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
             } else {
                 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    const float2 iv = *reinterpret_cast<const float2*>(inv + kb * TOK + 8 * a + 2 * t);
+                    const float2 iv = *reinterpret_cast<const float2*>(inv + kb * TOK + 8 * a + 2 * t);   // past M: unused
                     #pragma unroll
                     for (int T = 0; T < 2; ++T) {
                         tot[a][T][0] = fmaf(acc[a][T][0], iv.x, tot[a][T][0]);
