@@ -590,16 +590,19 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         __syncthreads();
     }
 
+    // SILU_BWD_CK: lane cl holds the gate scale of row R0 + cl (cl < 8) or the up scale of row
+    // R0 + cl - 8 of its half, requested an item ahead
+    auto ckpt_scale = [&](int it) {
+        int64_t pnl, tt;
+        tile_at(it, pnl, tt);
+        const int64_t m = pnl * 128 + R0 + (cl & 7);
+        return m < a.M ? __ldg(a.xs + (tt + (cl < 8 ? 0 : ntiles / 2)) * a.M + m) : 0.0f;
+    };
+    float ck_next = 0.0f;
+    if (PRO == PRO_SILU_BWD_CK && total > 0) ck_next = ckpt_scale(0);
     for (; ok && item < total; ++item) {
-        float ck_scale = 0.0f;
-        if (PRO == PRO_SILU_BWD_CK) {
-            // lane cl holds the gate scale of row R0 + cl (cl < 8) or the up scale of row
-            // R0 + cl - 8 of its half; requested before the wait for the item's tiles
-            int64_t pnl, tt;
-            tile_at(item, pnl, tt);
-            const int64_t m = pnl * 128 + R0 + (cl & 7);
-            if (m < a.M) ck_scale = __ldg(a.xs + (tt + (cl < 8 ? 0 : ntiles / 2)) * a.M + m);
-        }
+        const float ck_scale = ck_next;
+        if (PRO == PRO_SILU_BWD_CK && item + 1 < total) ck_next = ckpt_scale(item + 1);
         ok = wait_item(item);
         if (!ok) break;
         int64_t panel, t;
