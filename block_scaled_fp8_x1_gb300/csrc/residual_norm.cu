@@ -92,8 +92,12 @@ __device__ __forceinline__ void quant_groups(const uint4 (&v)[G], float* sp, uin
     }
 }
 
-// 1/sqrt(mean + eps) by the hardware's reciprocal square root (2 ulp).
-__device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) { return rsqrtf(fmaf(sumsq, inv_k, eps)); }
+// 1/sqrt(mean + eps): the hardware's reciprocal square root (2 ulp) and one step of Newton's method,
+// r + r (1 - v r^2) / 2, on its residual.  Infinite or zero v keeps the first value.
+__device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) {
+    const float v = fmaf(sumsq, inv_k, eps), r = rsqrtf(v), e = fmaf(-__fmul_rn(v, r), r, 1.0f);
+    return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+}
 
 }  // namespace
 
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const fp8rl_residu
         pre[i] = c < K ? ld_v4(a.pre_gamma + c) : zero;
         #pragma unroll
         for (int j = 0; j < 4; ++j)
-            s_w[(i * 4 + j) * nt + tid] = __fmul2_rn(__fmul2_rn(both(a.alpha), pair(word(g, j))), pair(word(p, j)));
+            s_w[(i * 4 + j) * nt + tid] = __fmul2_rn(both(a.alpha), __fmul2_rn(pair(word(g, j)), pair(word(p, j))));   // the inner product is exact
     }
     if (tid < 32) s_sum[0][tid] = s_sum[1][tid] = 0.0f;
     // groups of a half-warp: z's chunks, then h's, then y's; lane `me` stores the scale of group me
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
         const uint4 g = GATE && c < K ? ld_v4(a.gate + c) : one;
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            w[i][j] = __fmul2_rn(__fmul2_rn(both(a.alpha), pair(word(g, j))), pair(word(p, j)));
+            w[i][j] = __fmul2_rn(both(a.alpha), __fmul2_rn(pair(word(g, j)), pair(word(p, j))));   // the inner product is exact
             a_pre[i][j] = a_v[i][j] = both(0.0f);
         }
     }
