@@ -16,6 +16,12 @@
 //     dy     = r_y (u - y^ mean(u y^)),     u = dn g_post, y^ = y r_y       (or dy = dn)
 //     dg_pre = sum_m dz x^,  dg_post = sum_m dn y^,  dgate = sum_m alpha dH n
 // dH stays in FP32 between the two halves.
+//
+// What bounds them.  The forward moves 6 bytes an element in and out for h, y, h' and 1 to 2 more
+// for each form of z and each checkpoint: 16384 x 5120 to BF16 takes 102 us, 0.97 of the measured
+// copy rate; with z's codes and both checkpoints 149 us (0.76), bound by instruction issue (the
+// three encodes), and the 128x1 codes, a second kernel that reads h' again, 58 us more.  The
+// backward of the same size takes 158 us from BF16 (0.94) and 151 us from checkpoints (0.83).
 #include "block.h"
 #include "quant_common.cuh"
 

@@ -216,7 +216,8 @@ FP8RL_API fp8rl_status fp8rl_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const f
  *   n  = y r(y) g_post  (n = y when post_gamma is NULL),  r(v) = 1/sqrt(mean(v^2) + eps)
  *   h' = bf16_rne(h + alpha gate n)  (gate = 1 when NULL)
  *   z  = bf16_rne((h' r(h')) g_pre)
- * evaluated in FP32.  With post_gamma = gate = NULL and alpha = 1 this is the residual add
+ * evaluated in FP32 (the squares too: a row whose sum of squares leaves FP32's range has r = 0,
+ * as does one with an infinity; a NaN stays in its row).  With post_gamma = gate = NULL and alpha = 1 this is the residual add
  * and norm of a pre-norm block.  A row's result depends on that row alone: a token gives
  * the same bits in a batch of one and in a training batch.
  * -------------------------------------------------------------------------------------- */
