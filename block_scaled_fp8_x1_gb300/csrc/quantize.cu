@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(256) k_quant_1x128(const uint16_t* __restrict_
 // code tile and the tile's 128 row scales) for the 128x1 WGrad operand.
 // PRO_SILU_CK is PRO_SILU that also quantizes its gate and up tiles 1x128 (the 8-bit
 // checkpoint of the gate_up output): 227 us at 8192 x 14336 dual, 0.62 of the copy rate, where
-// SiLU-mul and the stand-alone quantizer take 147 + 200 us and read gu twice.  PRO_SILU_BWD_CK is
-// PRO_SILU_BWD from that checkpoint: 989 us at 16384 x 27648 dual (0.56; from BF16 1068 us).  Both
+// SiLU-mul and the stand-alone quantizer take 147 + 205 us and read gu twice.  PRO_SILU_BWD_CK is
+// PRO_SILU_BWD from that checkpoint: 989 us at 16384 x 27648 dual (0.56; from BF16 1061 us).  Both
 // are bound by instruction issue: three or four encodes and a sigmoid per element.
 enum Prologue : int { PRO_COPY = 0, PRO_SILU = 1, PRO_RMSNORM = 2, PRO_RMSNORM_G = 3, PRO_SILU_BWD = 5,
                       PRO_DEQUANT = 6, PRO_SILU_BWD_CK = 7, PRO_SILU_CK = 8 };

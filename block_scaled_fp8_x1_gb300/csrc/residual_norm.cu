@@ -113,7 +113,9 @@ __device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) {
 template <bool POST, bool Q, bool CK, int NCH, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const fp8rl_residual_norm_args a, int64_t M, int64_t K) {
     grid_dependency_begin();
-    extern __shared__ __align__(16) float2 s_w[];     // alpha * gate * g_post, [NCH][4 pairs][threads]
+    // gate * g_post (exact: two BF16 factors), [NCH][4 pairs][threads]; alpha is multiplied in last, so
+    // that without a post norm the branch takes the one rounding of alpha (gate y)
+    extern __shared__ __align__(16) float2 s_w[];
     __shared__ float s_sum[2][32];
     const int tid = threadIdx.x, nt = blockDim.x, me = tid & 15;
     const float inv_k = __fdiv_rn(1.0f, (float)K);
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const fp8rl_residu
         pre[i] = c < K ? ld_v4(a.pre_gamma + c) : zero;
         #pragma unroll
         for (int j = 0; j < 4; ++j)
-            s_w[(i * 4 + j) * nt + tid] = __fmul2_rn(both(a.alpha), __fmul2_rn(pair(word(g, j)), pair(word(p, j))));   // the inner product is exact
+            s_w[(i * 4 + j) * nt + tid] = __fmul2_rn(pair(word(g, j)), pair(word(p, j)));
     }
     if (tid < 32) s_sum[0][tid] = s_sum[1][tid] = 0.0f;
     // groups of a half-warp: z's chunks, then h's, then y's; lane `me` stores the scale of group me
@@ -178,7 +180,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_residual_norm(const fp8rl_residu
             uint32_t o[4];
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 x = __ffma2_rn(__fmul2_rn(pair(word(yv[i], j)), both(ry)), s_w[(i * 4 + j) * nt + tid], pair(word(hv[i], j)));
+                const float2 y = POST ? __fmul2_rn(pair(word(yv[i], j)), both(ry)) : pair(word(yv[i], j));
+                const float2 x = __fadd2_rn(__fmul2_rn(__fmul2_rn(y, s_w[(i * 4 + j) * nt + tid]), both(a.alpha)), pair(word(hv[i], j)));
                 o[j] = pack_bf16x2(x.x, x.y);
                 ss = __ffma2_rn(pair(o[j]), pair(o[j]), ss);
             }
