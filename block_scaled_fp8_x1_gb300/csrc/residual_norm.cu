@@ -19,7 +19,7 @@
 //
 // What bounds them.  The forward moves 6 bytes an element in and out for h, y, h' and 1 to 2 more
 // for each form of z and each checkpoint: 16384 x 5120 to BF16 takes 102 us, 0.97 of the measured
-// copy rate; with z's codes and both checkpoints 149 us (0.76), bound by instruction issue (the
+// copy rate; with z's codes and both checkpoints 153 us (0.74), bound by instruction issue (the
 // three encodes), and the 128x1 codes, a second kernel that reads h' again, 58 us more.  The
 // backward of the same size takes 158 us from BF16 (0.94) and 151 us from checkpoints (0.83).
 #include "block.h"
@@ -253,7 +253,7 @@ static cudaError_t launch_fwd(const fp8rl_residual_norm_args& a, int64_t M, int6
 cudaError_t launch_residual_norm(const fp8rl_residual_norm_args& a, int64_t M, int64_t K, int num_sms, cudaStream_t st) {
     // Two chunks of 8 columns a thread, as many CTAs on an SM as registers allow without spills
     // (the compiler's bound is for the widest row of each range).  16384 x 5120, BF16 out /
-    // quantized with both checkpoints, in us: 103 / 149 so, 117 / 166 with three CTAs at 64
+    // quantized with both checkpoints, in us: 103 / 153 so, 117 / 166 with three CTAs at 64
     // registers, 102 / 202 with one chunk and 640 threads, 114 / 172 with four chunks.
     if (K <= 2560) return launch_fwd<2, 160, 4>(a, M, K, num_sms, st);
     if (K <= 4096) return launch_fwd<2, 256, 3>(a, M, K, num_sms, st);
