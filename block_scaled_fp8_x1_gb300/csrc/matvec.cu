@@ -360,7 +360,8 @@ size_t matvec_smem(int M, int nkb, int splits) {
 cudaError_t launch_matvec_nvfp4(const MatvecParams& p, int clusters, cudaStream_t st) {
     const size_t smem = matvec_smem(p.M, p.nkb, p.splits);
     auto kern = p.M == 1 ? k_matvec_nvfp4<true, 1> : p.M <= 8 ? k_matvec_nvfp4<false, 1> : k_matvec_nvfp4<false, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // one limit for every call: host threads may launch different sizes at once
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMatvecMaxSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(clusters * p.splits)), block(kWarps * 32);
     // clusters are launched plainly: set up ahead of the previous kernel's end they ran 2 us later

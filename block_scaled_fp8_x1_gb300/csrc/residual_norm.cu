@@ -535,12 +535,13 @@ struct BwdShape {
     int nch, nt, slots, per_sm;
     size_t smem;
 };
+constexpr int kBwdMaxSmem = 200 * 1024;
 static BwdShape bwd_shape(int64_t K, bool ck) {
     BwdShape s;
     s.nch = K <= 8 * 640 ? 1 : 2;
     s.nt = norm_threads((K / 8 + s.nch - 1) / s.nch * 8);
     const size_t row = (size_t)s.nt * s.nch * (ck ? Slot<true>::BYTES : Slot<false>::BYTES);
-    s.slots = 4 * row <= 200 * 1024 ? 4 : 3;
+    s.slots = 4 * row <= kBwdMaxSmem ? 4 : 3;   // 8192 columns of BF16: 3 x 64 KB
     s.smem = (size_t)s.slots * row;
     s.per_sm = (s.nch == 1 ? 640 : 512) / s.nt;
     const int by_smem = (int)(216 * 1024 / (s.smem + 1536));
@@ -560,7 +561,8 @@ static cudaError_t launch_bwd_t(const fp8rl_residual_norm_bwd_args& a, int64_t M
                                 cudaStream_t st) {
     const BwdShape s = bwd_shape(K, CK);
     auto kern = s.nch == 1 ? k_residual_norm_bwd<POST, GATE, CK, 1> : k_residual_norm_bwd<POST, GATE, CK, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    // one limit for every call: host threads may launch different sizes at once
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdMaxSmem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, dim3(nb), dim3(s.nt), s.smem, st, a, M, K, s.slots, ws);
 }
