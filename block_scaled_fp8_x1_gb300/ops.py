@@ -295,7 +295,8 @@ class ResidualNormGrads(NamedTuple):
 
 def _rows(t: torch.Tensor, name: str, shape, device) -> int:
     """Checks a bf16 matrix of contiguous rows and returns its row stride."""
-    _require(t, torch.bfloat16, name, device)
+    if t.dtype is not torch.bfloat16 or t.device != device or not t.is_cuda:
+        _require(t, torch.bfloat16, name, device)
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     ld, step = t.stride()
@@ -307,10 +308,12 @@ def _rows(t: torch.Tensor, name: str, shape, device) -> int:
 def _vector(t: Optional[torch.Tensor], name: str, dtype, n: int, device) -> None:
     if t is None:
         return
-    _require(t, dtype, name, device)
-    if t.shape != (n,):
+    if t.dtype is not dtype or t.device != device or not t.is_cuda:
+        _require(t, dtype, name, device)
+    if t.dim() != 1 or t.numel() != n:
         raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(t.shape)}")
-    _contig(t, name)
+    if not t.is_contiguous():
+        _contig(t, name)
 
 
 def _codes(M: int, K: int, dev) -> Checkpoint:
@@ -339,8 +342,9 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, pre_gamma: torch.Tensor, eps
     shape, dev = h.shape, h.device
     M, K = shape
     ldh, ldy = _rows(h, "h", shape, dev), _rows(y, "y", shape, dev)
-    for t, n in ((pre_gamma, "pre_gamma"), (post_gamma, "post_gamma"), (gate, "gate")):
-        _vector(t, n, torch.bfloat16, K, dev)
+    _vector(pre_gamma, "pre_gamma", torch.bfloat16, K, dev)
+    _vector(post_gamma, "post_gamma", torch.bfloat16, K, dev)
+    _vector(gate, "gate", torch.bfloat16, K, dev)
     if emit not in ("bf16", "fp8", "dual"):
         raise ValueError(f"emit: expected 'bf16', 'fp8' or 'dual', got {emit!r}")
     if inplace and not h.is_contiguous():
@@ -356,14 +360,22 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, pre_gamma: torch.Tensor, eps
     if checkpoint:
         h_ckpt, y_ckpt = _codes(M, K, dev), _codes(M, K, dev)
     r_pre = torch.empty(M, dtype=torch.float32, device=dev)
+    args = _abi.ResidualNormArgs(h=h.data_ptr(), ldh=ldh, y=y.data_ptr(), ldy=ldy, pre_gamma=pre_gamma.data_ptr(),
+                                 alpha=float(alpha), eps=float(eps), h_out=h_out.data_ptr(), r_pre=r_pre.data_ptr())
     if post_gamma is not None:
         r_post = torch.empty(M, dtype=torch.float32, device=dev)
-    qh, sh = h_ckpt or (None, None)
-    qy, sy = y_ckpt or (None, None)
-    args = _abi.ResidualNormArgs(
-        _ptr(h), ldh, _ptr(y), ldy, _ptr(post_gamma), _ptr(gate), _ptr(pre_gamma), float(alpha), float(eps),
-        _ptr(h_out), _ptr(z), _ptr(q), _ptr(s), _ptr(qT), _ptr(sT), _ptr(qh), _ptr(sh), _ptr(qy), _ptr(sy),
-        _ptr(r_pre), _ptr(r_post))
+        args.post_gamma, args.r_post = post_gamma.data_ptr(), r_post.data_ptr()
+    if gate is not None:
+        args.gate = gate.data_ptr()
+    if z is not None:
+        args.z = z.data_ptr()
+    else:
+        args.q, args.s = q.data_ptr(), s.data_ptr()
+    if qT is not None:
+        args.qT, args.sT = qT.data_ptr(), sT.data_ptr()
+    if checkpoint:
+        args.qh, args.sh = map(_ptr, h_ckpt)
+        args.qy, args.sy = map(_ptr, y_ckpt)
     check(lib().fp8rl_residual_norm(ctypes.byref(args), M, K, _stream(dev)), "fp8rl_residual_norm")
     return ResidualNorm(h_out, z, q, s, qT, sT, r_pre, r_post, h_ckpt, y_ckpt)
 
@@ -397,8 +409,9 @@ def residual_norm_bwd(dz: torch.Tensor, dh: Optional[torch.Tensor], h: Union[tor
     dev = dz.device
     lddz = _rows(dz, "dz", (M, K), dev)
     lddh = _rows(dh, "dh", (M, K), dev) if dh is not None else 0
-    for t, n in ((pre_gamma, "pre_gamma"), (post_gamma, "post_gamma"), (gate, "gate")):
-        _vector(t, n, torch.bfloat16, K, dev)
+    _vector(pre_gamma, "pre_gamma", torch.bfloat16, K, dev)
+    _vector(post_gamma, "post_gamma", torch.bfloat16, K, dev)
+    _vector(gate, "gate", torch.bfloat16, K, dev)
     _vector(r_pre, "r_pre", torch.float32, M, dev)
     _vector(r_post, "r_post", torch.float32, M, dev)
     if post_gamma is not None and r_post is None:
