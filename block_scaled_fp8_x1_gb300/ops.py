@@ -342,6 +342,8 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor, pre_gamma: torch.Tensor, eps
     shape, dev = h.shape, h.device
     M, K = shape
     ldh, ldy = _rows(h, "h", shape, dev), _rows(y, "y", shape, dev)
+    if pre_gamma is None:
+        raise ValueError("pre_gamma: needed")
     _vector(pre_gamma, "pre_gamma", torch.bfloat16, K, dev)
     _vector(post_gamma, "post_gamma", torch.bfloat16, K, dev)
     _vector(gate, "gate", torch.bfloat16, K, dev)
@@ -409,6 +411,8 @@ def residual_norm_bwd(dz: torch.Tensor, dh: Optional[torch.Tensor], h: Union[tor
     dev = dz.device
     lddz = _rows(dz, "dz", (M, K), dev)
     lddh = _rows(dh, "dh", (M, K), dev) if dh is not None else 0
+    if pre_gamma is None or r_pre is None:
+        raise ValueError("pre_gamma, r_pre: needed")
     _vector(pre_gamma, "pre_gamma", torch.bfloat16, K, dev)
     _vector(post_gamma, "post_gamma", torch.bfloat16, K, dev)
     _vector(gate, "gate", torch.bfloat16, K, dev)

@@ -268,6 +268,8 @@ def test_refusals(fp8lib):
         fp8lib.residual_norm(h.t().contiguous().t(), y, pre, EPS)
     with pytest.raises(ValueError, match="pre_gamma"):
         fp8lib.residual_norm(h, y, pre[:128], EPS)
+    with pytest.raises(ValueError, match="pre_gamma"):
+        fp8lib.residual_norm(h, y, None, EPS)
     with pytest.raises(ValueError, match="emit"):
         fp8lib.residual_norm(h, y, pre, EPS, emit="int8")
     with pytest.raises(ValueError, match="on cpu|CUDA"):
