@@ -26,10 +26,9 @@
 // codes times x.  The scales then multiply 16 sums of a unit for a lane instead of its 128
 // weights, and the columns are added at the end.
 //
-// Why mma.sync: tcgen05.mma takes its weights from shared memory, in 16 bits here, so each decoded
-// weight would be written and read there, 4 bytes for its half byte from HBM: at the HBM rate (47
-// weights a cycle an SM) 188 bytes a cycle against the 128 that shared memory moves.  From registers
-// the same products cost 28 of the 98 cycles that HBM takes for a unit.
+// Why mma.sync: tcgen05.mma takes the weights from shared or tensor memory, so each decoded weight
+// would first be written there in 16 bits, four times its bytes from HBM, and read again.  From
+// registers the same products cost 28 of the 98 cycles that HBM takes for a unit (up to 8 tokens).
 //
 // A CTA of 16 warps (one on an SM, so that x is laid out once for all of them) works on 16 / WK
 // tiles of 32 rows at a time, WK warps splitting K, and a cluster

@@ -30,10 +30,6 @@ namespace fp8rl {
 namespace {
 
 __device__ __forceinline__ uint4 ld_v4(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ float elem(const uint4& v, int j) {
-    const uint32_t w = (j >> 1) == 0 ? v.x : (j >> 1) == 1 ? v.y : (j >> 1) == 2 ? v.z : v.w;
-    return (j & 1) ? bf16_hi(w) : bf16_lo(w);
-}
 
 // Sum of one value per thread over the CTA, the same in every thread: a shuffle tree in each
 // warp, then one over the warps' sums (buf[w], zero from nwarps up to 32).  Successive calls
