@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
     // (Odd tokens swap the slots' halves, so that two tokens of a load phase lie on other banks.)
     if (tid == 0) *reinterpret_cast<uint4*>(zeros) = make_uint4(0, 0, 0, 0);
     {
-        constexpr int XB = ONE ? 2 : 8;
+        constexpr int XB = ONE ? 2 : 6;
         const int l = tid & 15, items = kslice * p.M;
         uint4 xv[XB];
         auto load_x = [&](int it0) {
