@@ -1026,12 +1026,12 @@ fp8rl_status fp8rl_gemm_nvfp4(const uint8_t* qx, const uint8_t* sfx, const float
 // to 16 tokens, every split timed: the choice is within 4% of the fastest there (3584 x 3584 at 16
 // tokens: 9.5 us in clusters of 5, 12.0 us without; 14336 x 4096 at one: 10.7 us in one round of
 // four warps a tile, 12.1 us in three rounds of 16).
-static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_req, int* splits, int* wk, int* clusters) {
+static void matvec_plan(int M, bool one, int64_t nkb, int64_t tiles, int sms, int splits_req, int* splits, int* wk, int* clusters) {
     int best_s = 0, best_w = 1;
     double best = 1e30;
     for (int s = 1; s <= 8; ++s) {
         if (splits_req > 0 && s != splits_req) continue;
-        if (s > nkb || matvec_smem(M, (int)nkb, s) > kMatvecMaxSmem) continue;
+        if (s > nkb || matvec_smem(M, (int)nkb, s, one) > kMatvecMaxSmem) continue;
         for (int w = 1; w <= kMatvecWarps; w *= 2) {
             const int64_t per = kMatvecWarps / w, groups = (tiles + per - 1) / per, at_once = sms / s;
             const int64_t rounds = (groups + at_once - 1) / at_once;
@@ -1052,6 +1052,14 @@ static void matvec_plan(int M, int64_t nkb, int64_t tiles, int sms, int splits_r
     *clusters = (int)std::min<int64_t>(groups, best_s > 1 ? groups : (int64_t)sms);
 }
 
+// Whether M tokens' slices of K fit in shared memory, in the form of several tokens, whose shorter
+// ring leaves a single token more room than its own form does: from 2 tokens to 8, and from 9
+// to 16, more tokens need more, so that where M (2 to 8) fit, fewer do.
+static bool matvec_fits(int M, int64_t nkb, int splits_req) {
+    const int s = splits_req > 0 ? splits_req : (int)std::min<int64_t>(8, nkb);
+    return s <= nkb && matvec_smem(M, (int)nkb, s, false) <= kMatvecMaxSmem;
+}
+
 fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
                                 const uint8_t* sfw, const float* gw, int64_t N, uint16_t* y, int64_t ldy, int splits,
                                 fp8rl_stream_t stream) {
@@ -1061,20 +1069,28 @@ fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t
     if (!x || !qw || !sfw || !gw || !y) return FP8RL_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(qw) || !aligned16(sfw) || !aligned16(gw) || !aligned16(y) || ldx % 8 != 0 || ldy % 8 != 0)
         return FP8RL_ERR_ALIGN;
+    // tokens per launch: fewer where their slices of x would not fit in shared memory.  The
+    // last launch has no more than the others, so all of them fit or none is made.
+    const int64_t nkb = K / 128;
+    int64_t step = M;
+    while (step > 1 && !matvec_fits((int)step, nkb, splits)) step = (step + 1) / 2;
+    if (!matvec_fits((int)step, nkb, splits)) return FP8RL_ERR_SHAPE;   // not even one token
     int sms = 0;
     fp8rl_status e = current_device(&sms);
     if (e != FP8RL_OK) return e;
-    // tokens per launch: fewer where their slice of x would not fit in shared memory
-    int64_t step = M;
-    while (step > 1 && matvec_smem((int)step, (int)(K / 128), splits > 0 ? splits : 8) > kMatvecMaxSmem) step = (step + 1) / 2;
     for (int64_t m = 0; m < M; m += step) {
         MatvecParams p = {};
         p.M = (int)std::min(step, M - m);
-        p.nkb = (int)(K / 128);
+        p.nkb = (int)nkb;
         p.tiles = (int)(N / 32);
         int clusters = 0;
-        matvec_plan(p.M, p.nkb, p.tiles, sms, splits, &p.splits, &p.wk, &clusters);
-        if (p.splits == 0) return FP8RL_ERR_SHAPE;   // one token's slice of K does not fit
+        p.one = p.M == 1;
+        matvec_plan(p.M, p.one, nkb, p.tiles, sms, splits, &p.splits, &p.wk, &clusters);
+        if (p.splits == 0 && p.one) {   // K too long for the one-token form's ring
+            p.one = false;
+            matvec_plan(p.M, p.one, nkb, p.tiles, sms, splits, &p.splits, &p.wk, &clusters);
+        }
+        if (p.splits == 0) return FP8RL_ERR_SHAPE;
         p.x = x + m * ldx;
         p.ldx = ldx;
         p.qw = qw;

@@ -33,6 +33,7 @@ cudaError_t launch_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const float* sgu,
 // matvec.cu: y = x W^T for M <= 16 BF16 tokens, W in NVFP4 (codes, scale atoms, row scales).
 struct MatvecParams {
     int M;                   // tokens, 1..16
+    bool one;                // the one-token form (M == 1)
     int nkb;                 // K / 128 (even)
     int tiles;               // N / 32 (a multiple of 4)
     int splits;              // CTAs of a cluster that share K, 1..8
@@ -48,7 +49,7 @@ struct MatvecParams {
 constexpr int kMatvecMaxTokens = 16;
 constexpr int kMatvecWarps = 16;
 constexpr size_t kMatvecMaxSmem = 224 * 1024;
-size_t matvec_smem(int M, int nkb, int splits);   // dynamic shared memory of a CTA
+size_t matvec_smem(int M, int nkb, int splits, bool one);   // dynamic shared memory of a CTA
 // `clusters` of p.splits CTAs, each taking every clusters-th group of kMatvecWarps / wk tiles of
 // 32 rows.
 cudaError_t launch_matvec_nvfp4(const MatvecParams& p, int clusters, cudaStream_t st);

@@ -104,7 +104,8 @@ struct Unit {
 
 }  // namespace
 
-// ONE: a single token (NT = 1); else NT groups of 8 tokens.
+// ONE: a single token (NT = 1); else NT groups of 8 tokens, a single one too where K is too long for
+// the deeper ring of its own form.
 template <bool ONE, int NT>
 __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecParams p) {
     grid_dependency_begin();
@@ -356,14 +357,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
     cp_async_wait_all();
 }
 
-size_t matvec_smem(int M, int nkb, int splits) {
-    const int tok = M == 1 ? 1 : (M + 7) / 8 * 8, kmax = (nkb + splits - 1) / splits;
-    return (size_t)kWarps * depth_of(M == 1, tok / 8) * kUnit + 16 + (size_t)kmax * M * kXBlock + (((size_t)kmax * tok + 3) & ~(size_t)3) * 4 + (size_t)kWarps * tok * 32 * 4;
+size_t matvec_smem(int M, int nkb, int splits, bool one) {
+    const int tok = one ? 1 : (M + 7) / 8 * 8, kmax = (nkb + splits - 1) / splits;
+    return (size_t)kWarps * depth_of(one, tok / 8) * kUnit + 16 + (size_t)kmax * M * kXBlock + (((size_t)kmax * tok + 3) & ~(size_t)3) * 4 + (size_t)kWarps * tok * 32 * 4;
 }
 
 cudaError_t launch_matvec_nvfp4(const MatvecParams& p, int clusters, cudaStream_t st) {
-    const size_t smem = matvec_smem(p.M, p.nkb, p.splits);
-    auto kern = p.M == 1 ? k_matvec_nvfp4<true, 1> : p.M <= 8 ? k_matvec_nvfp4<false, 1> : k_matvec_nvfp4<false, 2>;
+    const size_t smem = matvec_smem(p.M, p.nkb, p.splits, p.one);
+    auto kern = p.one ? k_matvec_nvfp4<true, 1> : p.M <= 8 ? k_matvec_nvfp4<false, 1> : k_matvec_nvfp4<false, 2>;
     // one limit for every call: host threads may launch different sizes at once
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMatvecMaxSmem);
     if (e != cudaSuccess) return e;

@@ -487,8 +487,9 @@ FP8RL_API fp8rl_status fp8rl_linear_nvfp4(const uint16_t* x, int64_t M, int64_t 
  *   y : BF16 [M][ldy], ldy >= N, ldy % 8 == 0.  0 <= M <= 16, N % 128 == 0, K % 256 == 0.
  * splits: CTAs of a cluster that share the reduction (1..8; 0 = automatic).  A token's result
  * may differ in its last bit between calls of different M.  No workspace, one launch
- * (more only when K is so long that the tokens' x does not fit in shared memory at once:
- * FP8RL_ERR_SHAPE when a single token's does not). */
+ * (more only when K is so long that the tokens' x does not fit in shared memory at once).  A K
+ * so long that one token's slice does not fit, above 45440 for each CTA that shares it, is
+ * FP8RL_ERR_SHAPE for every M, before anything is launched.  y overlaps nothing. */
 FP8RL_API fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
                                           const uint8_t* qw, const uint8_t* sfw, const float* gw,
                                           int64_t N, uint16_t* y, int64_t ldy, int splits,
