@@ -1057,7 +1057,7 @@ static void matvec_plan(int M, bool one, int64_t nkb, int64_t tiles, int sms, in
 // to 16, more tokens need more, so that where M (2 to 8) fit, fewer do.
 static bool matvec_fits(int M, int64_t nkb, int splits_req) {
     const int s = splits_req > 0 ? splits_req : (int)std::min<int64_t>(8, nkb);
-    return s <= nkb && matvec_smem(M, (int)nkb, s, false) <= kMatvecMaxSmem;
+    return matvec_smem(M, (int)nkb, s, false) <= kMatvecMaxSmem;
 }
 
 fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw,
@@ -1072,6 +1072,7 @@ fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t
     // tokens per launch: fewer where their slices of x would not fit in shared memory.  The
     // last launch has no more than the others, so all of them fit or none is made.
     const int64_t nkb = K / 128;
+    splits = (int)std::min<int64_t>(splits, nkb);
     int64_t step = M;
     while (step > 1 && !matvec_fits((int)step, nkb, splits)) step = (step + 1) / 2;
     if (!matvec_fits((int)step, nkb, splits)) return FP8RL_ERR_SHAPE;   // not even one token

@@ -485,7 +485,8 @@ FP8RL_API fp8rl_status fp8rl_linear_nvfp4(const uint16_t* x, int64_t M, int64_t 
  * bits) and are summed in FP32 in a fixed order.
  *   x : BF16 [M][ldx], ldx >= K, ldx % 8 == 0;  qw / sfw / gw as fp8rl_quantize_nvfp4 of W [N][K];
  *   y : BF16 [M][ldy], ldy >= N, ldy % 8 == 0.  0 <= M <= 16, N % 128 == 0, K % 256 == 0.
- * splits: CTAs of a cluster that share the reduction (1..8; 0 = automatic).  A token's result
+ * splits: CTAs of a cluster that share the reduction (1..8, or as many as K / 128 where that is
+ * fewer; 0 = automatic).  A token's result
  * may differ in its last bit between calls of different M.  No workspace, one launch
  * (more only when K is so long that the tokens' x does not fit in shared memory at once).  A K
  * so long that one token's slice does not fit, above 45440 for each CTA that shares it, is
