@@ -10,7 +10,9 @@
 // and 128 elements of K that takes their largest magnitude to [2^14, 2^15): its 8 significant bits
 // fit, and only what is below 2^-28 of that maximum loses bits (an error below 2^-39 of it).  So
 // the products are those of the given numbers and the FP16 tensor-core MMA sums them in FP32; the
-// scale comes off in FP32, exactly.
+// scale comes off in FP32, exactly.  There the row's g goes in as well, as far as it is a power of two
+// (its fraction multiplies the finished sum): g is the row's largest weight / 2688, and sums in units
+// of it would pass FP32's largest number where the result is 10^-4 of that.
 //
 // Work.  A unit is 32 weight rows x 128 of K: 2 KB of codes and 256 B of scales, which one warp
 // copies to its own ring in shared memory (DEPTH units ahead) and multiplies with mma.m16n8k16:
@@ -97,6 +99,12 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// The power of two in a row scale, 2^-64 to 2^64, and its inverse: the sums run in units of what is
+// left of the scale, so that they leave FP32's range only where the result does.
+__device__ __forceinline__ uint32_t scale_exponent(float g) { return min(max(__float_as_uint(g) >> 23 & 255u, 63u), 191u); }
+__device__ __forceinline__ float scale_power(float g) { return __uint_as_float(scale_exponent(g) << 23); }
+__device__ __forceinline__ float scale_rest(float g) { return g * __uint_as_float((254u - scale_exponent(g)) << 23); }
+
 struct Unit {
     uint4 w[4];   // codes of rows 8o + g + 32 i, K = 32t .. 32t + 31
     uint4 sf;     // their scale atom row: word i = row i's four scales of 64 elements
@@ -151,6 +159,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
         cp_slot = cp_slot + 1 == DEPTH ? 0 : cp_slot + 1;
         cp_async_commit();
     };
+
+    // the scales of this lane's four rows of the warp's next tile, requested a tile ahead
+    float g_next[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    auto load_g = [&](int tile) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (tile < ntile) g_next[i] = p.gw[(int64_t)(tile >> 2) * 128 + 32 * i + 8 * (tile & 3) + g];
+    };
+    load_g(cl * per + wt);
 
     // x to FP16 in fragment order: 16 lanes take one (K-block, token) block of 128.  Lane l holds
     // elements 8l .. 8l + 7, that is lane t = l / 4 of the MMA, quarter jj = l % 4: slot 4 jj + t.
@@ -214,6 +231,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
     int slot = 0;
     for (int tile0 = cl * per; tile0 < ntile; tile0 += ncl * per) {
         const int tile = tile0 + wt;
+        float gp[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) gp[i] = scale_power(g_next[i]);
+        load_g(tile + ncl * per);
         float tot[NT][2][4];
         #pragma unroll
         for (int a = 0; a < NT; ++a)
@@ -275,19 +296,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
                 for (int i = 0; i < 4; ++i) {
                     const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sc[i]));
                     const float v = fmaf(acc[0][i >> 1][2 * (i & 1)], s.x, acc[0][i >> 1][2 * (i & 1) + 1] * s.y);
-                    tot[0][0][i] = fmaf(v, iv, tot[0][0][i]);
+                    tot[0][0][i] = fmaf(v * gp[i], iv, tot[0][0][i]);
                 }
             } else {
                 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
                     const float2 iv = *reinterpret_cast<const float2*>(inv + kb * TOK + 8 * a + 2 * t);   // past M: unused
                     #pragma unroll
-                    for (int T = 0; T < 2; ++T) {
-                        tot[a][T][0] = fmaf(acc[a][T][0], iv.x, tot[a][T][0]);
-                        tot[a][T][1] = fmaf(acc[a][T][1], iv.y, tot[a][T][1]);
-                        tot[a][T][2] = fmaf(acc[a][T][2], iv.x, tot[a][T][2]);
-                        tot[a][T][3] = fmaf(acc[a][T][3], iv.y, tot[a][T][3]);
-                    }
+                    for (int T = 0; T < 2; ++T)
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {        // rows 2T and 2T + 1, columns 2t and 2t + 1
+                            const float2 v = __fmul2_rn(make_float2(acc[a][T][2 * i], acc[a][T][2 * i + 1]), make_float2(gp[2 * T + i], gp[2 * T + i]));
+                            const float2 s = __ffma2_rn(v, iv, make_float2(tot[a][T][2 * i], tot[a][T][2 * i + 1]));
+                            tot[a][T][2 * i] = s.x;
+                            tot[a][T][2 * i + 1] = s.y;
+                        }
                 }
             }
         };
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_matvec_nvfp4(const MatvecPar
                 }
             }
             const int64_t n = (int64_t)(tl >> 2) * 128 + 32 * (r >> 3) + 8 * (tl & 3) + (r & 7);
-            p.y[(int64_t)m * p.ldy + n] = (uint16_t)(pack_bf16x2(v * p.gw[n], 0.0f) & 0xFFFFu);
+            p.y[(int64_t)m * p.ldy + n] = (uint16_t)(pack_bf16x2(v * scale_rest(p.gw[n]), 0.0f) & 0xFFFFu);
         }
         // the next tiles' parts (or the exit of a CTA whose parts are still read)
         __syncwarp();

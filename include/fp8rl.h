@@ -482,7 +482,8 @@ FP8RL_API fp8rl_status fp8rl_linear_nvfp4(const uint16_t* x, int64_t M, int64_t 
 /* The same linear for 1 to 16 tokens with the activation left in BF16: only the weights are in
  * 4 bits.  y[m][n] = bf16_rne(gw[n] sum_k x[m][k] w^(n,k)), w^ the code times its block scale;
  * the products are exact (an element below 2^-28 of the largest of its 128 neighbours may lose
- * bits) and are summed in FP32 in a fixed order.
+ * bits) and are summed in FP32 in a fixed order, in units of the fraction of gw[n] (its power of
+ * two goes into the sum: a partial sum leaves FP32's range only where y's terms do).
  *   x : BF16 [M][ldx], ldx >= K, ldx % 8 == 0;  qw / sfw / gw as fp8rl_quantize_nvfp4 of W [N][K];
  *   y : BF16 [M][ldy], ldy >= N, ldy % 8 == 0.  0 <= M <= 16, N % 128 == 0, K % 256 == 0.
  * splits: CTAs of a cluster that share the reduction (1..8, or as many as K / 128 where that is
