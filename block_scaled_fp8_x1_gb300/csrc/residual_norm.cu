@@ -94,10 +94,13 @@ __device__ __forceinline__ void quant_groups(const uint4 (&v)[G], float* sp, uin
     }
 }
 
-// 1/sqrt(mean + eps): the hardware's reciprocal square root (2 ulp) and one step of Newton's method,
-// r + r (1 - v r^2) / 2, on its residual.  Infinite or zero v keeps the first value.
+// 1/sqrt(mean + eps): the hardware's reciprocal square root r (2 ulp) and one step of Newton's method,
+// r + r (1 - v r^2) / 2, with the rounding error of v r in the residual, so that the result is v's
+// root rounded once (without it, off by up to one unit in the last place).  Infinite or zero v keeps the
+// first value.
 __device__ __forceinline__ float rstd_of(float sumsq, float inv_k, float eps) {
-    const float v = fmaf(sumsq, inv_k, eps), r = rsqrtf(v), e = fmaf(-__fmul_rn(v, r), r, 1.0f);
+    const float v = fmaf(sumsq, inv_k, eps), r = rsqrtf(v), p = __fmul_rn(v, r);
+    const float e = fmaf(-fmaf(v, r, -p), r, fmaf(-p, r, 1.0f));
     return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
 }
 

@@ -217,7 +217,10 @@ FP8RL_API fp8rl_status fp8rl_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const f
  *   h' = bf16_rne(h + alpha gate n)  (gate = 1 when NULL)
  *   z  = bf16_rne((h' r(h')) g_pre)
  * evaluated in FP32 (the squares too: a row whose sum of squares leaves FP32's range has r = 0,
- * as does one with an infinity; a NaN stays in its row).  With post_gamma = gate = NULL and alpha = 1 this is the residual add
+ * as does one with an infinity; a NaN stays in its row; with eps = 0 a row of zeros has an infinite r).
+ * The squares are added in FP32 without the error term that fp8rl_rmsnorm_quant's sum carries:
+ * r is within 2^-20 of its value, here as there a unit in the last place or so, and the two operators' r of one row
+ * may differ in the last bit.  With post_gamma = gate = NULL and alpha = 1 this is the residual add
  * and norm of a pre-norm block.  A row's result depends on that row alone: a token gives
  * the same bits in a batch of one and in a training batch.
  * -------------------------------------------------------------------------------------- */
