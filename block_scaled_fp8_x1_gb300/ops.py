@@ -22,10 +22,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr() if t is not None else None
 
 
+# the handle alone, where this torch has the call: the stream object that torch.cuda.current_stream
+# builds costs 2 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device):
-    # the handle alone: the stream object that torch.cuda.current_stream builds costs 2 us
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
     index = device.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    return _raw_stream(torch.cuda.current_device() if index is None else index)
 
 
 def _require(t: torch.Tensor, dtype: torch.dtype, name: str, device=None) -> None:
