@@ -1024,8 +1024,8 @@ fp8rl_status fp8rl_gemm_nvfp4(const uint8_t* qx, const uint8_t* sfx, const float
 // per round of tiles 1.2 for the CTA's own reduction or 1.8 + 0.15 S for a cluster's, plus 0.2 for each
 // pair of a token's blocks that its warp lays out.  Fitted on the 7B linears and 14336 x 4096, one
 // to 16 tokens, every split timed: the choice is within 4% of the fastest there (3584 x 3584 at 16
-// tokens: 9.5 us in clusters of 5, 12.0 us without; 14336 x 4096 at one: 10.7 us in one round of
-// four warps a tile, 12.1 us in three rounds of 16).
+// tokens: 9.6 us in clusters of 5, 12.0 us without; 14336 x 4096 at one: 10.0 us in one round of
+// four warps a tile; in three rounds of 16 it was 1.4 us slower).
 static void matvec_plan(int M, bool one, int64_t nkb, int64_t tiles, int sms, int splits_req, int* splits, int* wk, int* clusters) {
     int best_s = 0, best_w = 1;
     double best = 1e30;

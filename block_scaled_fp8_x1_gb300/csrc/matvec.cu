@@ -38,9 +38,11 @@
 // (distributed) shared memory.
 //
 // What bounds it.  One token on 37888 x 3584 (76 MB of weights): 17.2 us, 0.66 of the measured copy
-// rate; reading the same pieces and doing nothing takes 14.4 us.  Eight tokens 20.9, sixteen 28.4 us:
+// rate; reading the same pieces and doing nothing takes 14.4 us.  Eight tokens 20.8, sixteen 28.6 us:
 // there the decoding (64 conversions and 64 multiplies a unit and lane, two of either a cycle an SM)
-// and the 16 or 32 MMAs weigh more than the bytes.  3584 x 3584: 4.8 us, latency.
+// and the 16 or 32 MMAs weigh more than the bytes.  Less than half of the issue slots are used in any of
+// them: a unit is a chain of decoding, products and sums, and there are 16 warps.  3584 x 3584: 4.9 us,
+// latency.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -19,8 +19,8 @@
 //
 // What bounds them.  The forward moves 6 bytes an element in and out for h, y, h' and 1 to 2 more
 // for each form of z and each checkpoint: 16384 x 5120 to BF16 takes 102 us, 0.97 of the measured
-// copy rate; with z's codes and both checkpoints 153 us (0.74), bound by instruction issue (the
-// three encodes), and the 128x1 codes, a second kernel that reads h' again, 58 us more.  The
+// copy rate; with z's codes and both checkpoints 153 us (0.74), with 63% of the issue slots used: the
+// three encodes are dependent chains and 20 warps an SM do not fill their gaps; and the 128x1 codes, a second kernel that reads h' again, 58 us more.  The
 // backward of the same size takes 158 us from BF16 (0.94) and 151 us from checkpoints (0.83).
 #include "block.h"
 #include "quant_common.cuh"
@@ -326,7 +326,9 @@ __device__ __forceinline__ void saved_times(uint32_t words, float f, float2 (&x)
 // With w = alpha gate g_post, u = w dH and v = dH y^: mean(u y^) = mean(w v), and the two column
 // sums over the branch are multiples of one, V = sum_m v: dgate = alpha g_post V and
 // dg_post = alpha gate V.  So a thread keeps two sums for a column, dg_pre and V, in registers over
-// its rows; ws[b][0..1][K] takes them, and k_resnorm_colsum adds the blocks in order.
+// its rows; ws[b][0..1][K] takes them, and k_resnorm_colsum adds the blocks in order.  The sums are
+// plain FP32 (error terms would be 16 registers more a thread, past what 640 threads have): a block
+// has M / 152 rows or fewer, so a chain grows with M, by 2^-24 of its terms' magnitudes a row at most.
 template <bool POST, bool GATE, bool CK, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
     k_residual_norm_bwd(const fp8rl_residual_norm_bwd_args a, int64_t M, int64_t K, int slots, float* __restrict__ ws) {
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 640 : 512, 1)
 // block order, then the slices in order.
 __global__ void __launch_bounds__(256) k_resnorm_colsum(const fp8rl_residual_norm_bwd_args a, const float* __restrict__ ws,
                                                         int nblocks, int64_t K) {
-    grid_dependency_begin();   // launched while the rows are still worked on
+    grid_dependency_begin();   // set up as the row kernel ends; its sums are visible from here on
     __shared__ float part[8][33];
     const int x = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t k = (int64_t)blockIdx.x * 32 + x;

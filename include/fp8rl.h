@@ -219,8 +219,8 @@ FP8RL_API fp8rl_status fp8rl_silu_mul_bwd_quant_ckpt(const uint8_t* qgu, const f
  * evaluated in FP32 (the squares too: a row whose sum of squares leaves FP32's range has r = 0,
  * as does one with an infinity; a NaN stays in its row; with eps = 0 a row of zeros has an infinite r).
  * The squares are added in FP32 without the error term that fp8rl_rmsnorm_quant's sum carries:
- * r is within 2^-20 of its value, here as there a unit in the last place or so, and the two operators' r of one row
- * may differ in the last bit.  With post_gamma = gate = NULL and alpha = 1 this is the residual add
+ * r is within 2^-20 of its value (a unit or two in the last place on ordinary rows, as
+ * there), and the two operators' r of one row may differ in the last bits.  With post_gamma = gate = NULL and alpha = 1 this is the residual add
  * and norm of a pre-norm block.  A row's result depends on that row alone: a token gives
  * the same bits in a batch of one and in a training batch.
  * -------------------------------------------------------------------------------------- */
@@ -255,7 +255,8 @@ FP8RL_API fp8rl_status fp8rl_residual_norm(const fp8rl_residual_norm_args* args,
  *   (dy = dn without a post norm)
  *   dpre = sum_m dz x^,  dpost = sum_m dn y^,  dgate = sum_m alpha dH n
  * dh_out = bf16(dH) is the gradient of h.  dpost is written with post_gamma, dgate with gate.
- * The sums run in a fixed order: repeated calls give the same bits.  Every output overlaps
+ * The sums run in a fixed order: repeated calls give the same bits.  The column sums are plain FP32
+ * sums of M / 152 rows or fewer at a time (fp8rl_rmsnorm_bwd's carry an error term).  Every output overlaps
  * nothing.  ws: fp8rl_residual_norm_bwd_workspace_bytes(M, K), no initial contents. */
 typedef struct {
     const uint16_t* dz; int64_t lddz;  /* BF16 [M][lddz] */
