@@ -70,6 +70,26 @@ class ResidualNormBwdArgs(ctypes.Structure):
                 ("r_post", P), ("dh_out", P), ("dy", P), ("dpre", P), ("dpost", P), ("dgate", P)]
 
 
+INT = ctypes.c_int
+FP8RL_SCORE_SOFTMAX, FP8RL_SCORE_SIGMOID = 0, 1
+
+
+class RouteArgs(ctypes.Structure):
+    _fields_ = [("logits", P), ("ld", I64), ("bf16", INT), ("score", INT), ("bias", P), ("k", INT), ("n_groups", INT),
+                ("top_groups", INT), ("group_rank", INT), ("renormalize", INT), ("scale", F32), ("weight", P),
+                ("index", P)]
+
+
+class RouteBwdArgs(ctypes.Structure):
+    _fields_ = [("dweight", P), ("logits", P), ("ld", I64), ("bf16", INT), ("score", INT), ("index", P), ("k", INT),
+                ("renormalize", INT), ("scale", F32), ("dlogits", P), ("ldd", I64)]
+
+
+class ExpertLayout(ctypes.Structure):
+    _fields_ = [("pos", P), ("src", P), ("start", P), ("count", P), ("T", I64), ("k", I64), ("E", I64), ("R", I64),
+                ("align", I64)]
+
+
 ST = ctypes.c_int
 STREAM = ctypes.c_void_p
 
@@ -115,6 +135,17 @@ SIGNATURES = {
     "fp8rl_gemm_nvfp4": (ST, [P, P, P, P, P, P, P, I64, I64, I64, I64, ctypes.c_int, STREAM]),
     "fp8rl_linear_nvfp4": (ST, [P, I64, I64, I64, P, P, P, I64, P, P, P, P, STREAM]),
     "fp8rl_matvec_nvfp4": (ST, [P, I64, I64, I64, P, P, P, I64, P, I64, ctypes.c_int, STREAM]),
+    "fp8rl_route_topk": (ST, [ctypes.POINTER(RouteArgs), I64, I64, STREAM]),
+    "fp8rl_route_topk_bwd": (ST, [ctypes.POINTER(RouteBwdArgs), I64, I64, STREAM]),
+    "fp8rl_expert_rows_capacity": (I64, [I64, I64, I64, I64]),
+    "fp8rl_expert_rows": (ST, [P, I64, I64, I64, I64, P, P, P, P, P, ctypes.c_size_t, STREAM]),
+    "fp8rl_expert_rows_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64]),
+    "fp8rl_expert_gather_quant": (ST, [P, I64, I64, P, ctypes.POINTER(ExpertLayout), P, P, P, P, STREAM]),
+    "fp8rl_expert_combine": (ST, [P, I64, I64, P, P, I64, ctypes.POINTER(ExpertLayout), P, I64, STREAM]),
+    "fp8rl_expert_combine_dweight": (ST, [P, I64, P, I64, I64, ctypes.POINTER(ExpertLayout), P, STREAM]),
+    "fp8rl_gemm_experts_fwd": (ST, [P, P, P, P, P, I64, I64, ctypes.POINTER(ExpertLayout), STREAM]),
+    "fp8rl_gemm_experts_dgrad": (ST, [P, P, P, P, P, I64, I64, ctypes.POINTER(ExpertLayout), STREAM]),
+    "fp8rl_gemm_experts_wgrad": (ST, [P, P, P, P, P, I64, I64, ctypes.POINTER(ExpertLayout), STREAM]),
     "fp8rl_debug_e4m3_encode": (ST, [P, P, I64, STREAM]),
     "fp8rl_debug_e2m1_encode": (ST, [P, P, I64, STREAM]),
     "fp8rl_debug_encode_check": (ST, [ctypes.c_uint32, ctypes.c_uint32, P, P, STREAM]),

@@ -10,6 +10,7 @@
 
 #include "../../include/fp8rl.h"
 #include "block.h"
+#include "experts.h"
 #include "gemm.h"
 #include "rollout.h"
 
@@ -557,10 +558,14 @@ fp8rl_status fp8rl_check_status(fp8rl_stream_t stream) {
     const fp8rl_status dc = read_and_clear_decode_status();
     const fp8rl_status mc = read_and_clear_mc_status();
     const fp8rl_status nv = read_and_clear_nvf4_status();
+    const fp8rl_status xg = read_and_clear_experts_status();
+    const fp8rl_status xd = read_and_clear_decode_experts_status();
     if (g != FP8RL_OK) return g;
     if (pr != FP8RL_OK) return pr;
     if (mc != FP8RL_OK) return mc;
     if (nv != FP8RL_OK) return nv;
+    if (xg != FP8RL_OK) return xg;
+    if (xd != FP8RL_OK) return xd;
     return dc != FP8RL_OK ? dc : q;
 }
 
@@ -1154,6 +1159,256 @@ fp8rl_status fp8rl_gemm_fwd_decode_noalloc(const uint8_t* qx, const float* sx, c
 }
 
 size_t fp8rl_gemm_noalloc_scratch_bytes(void) { return noalloc_scratch_bytes(); }
+
+// ---------------------------------------------------------------- expert layers
+
+namespace {
+
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+bool expert_sizes(int64_t T, int64_t k, int64_t E, int64_t align) {
+    return T >= 0 && k >= 1 && k <= kMaxTopK && E >= 1 && E <= kMaxExperts && (align == 1 || align == kExpertAlign) &&
+           T <= kMaxPairs / k;
+}
+
+// A layout's sizes and arrays (those that `needs` names: p os, s rc, b egin, c ount).
+fp8rl_status check_layout(const fp8rl_expert_layout* l, const char* needs) {
+    if (!l || l->T < 0 || l->k < 1 || l->E < 1) return FP8RL_ERR_INVALID_ARG;
+    if (!expert_sizes(l->T, l->k, l->E, l->align)) return FP8RL_ERR_SHAPE;
+    if (l->R != fp8rl_expert_rows_capacity(l->T, l->k, l->E, l->align)) return FP8RL_ERR_SHAPE;
+    if (l->T == 0) return FP8RL_OK;
+    for (const char* c = needs; *c; ++c) {
+        const int32_t* p = *c == 'p' ? l->pos : *c == 's' ? l->src : *c == 'b' ? l->start : l->count;
+        if (!p) return FP8RL_ERR_INVALID_ARG;
+        if (!aligned_to(p, *c == 's' ? 16 : 4)) return FP8RL_ERR_ALIGN;
+    }
+    return FP8RL_OK;
+}
+
+// N and K of expert weights: multiples of 128, and coordinates of the stacked matrix that fit 31 bits.
+fp8rl_status check_expert_weights(int64_t N, int64_t K, int64_t E) {
+    if (N <= 0 || K <= 0) return FP8RL_ERR_INVALID_ARG;
+    if (N % 128 != 0 || K % 128 != 0) return FP8RL_ERR_SHAPE;
+    const int64_t most = int64_t(1) << 30;
+    return N > most / E || K > most ? FP8RL_ERR_SHAPE : FP8RL_OK;
+}
+
+// The products of align 128: A codes [R1][Kr] (rows in expert order, or WGrad's [N][R]).
+struct ExpertArgs {
+    const uint8_t* a; const float* sa;
+    const uint8_t* b; const float* sb;
+    uint16_t* c;
+    int64_t N, K;
+};
+
+fp8rl_status run_gemm_experts(ExpertOp op, const ExpertArgs& g, const fp8rl_expert_layout& l, int num_sms, cudaStream_t st) {
+    const bool wgrad = op == EXPERT_WGRAD;
+    const int64_t kr = op == EXPERT_FWD ? g.K : op == EXPERT_DGRAD ? g.N : l.R;        // stored reduction length
+    const int64_t cols = op == EXPERT_FWD ? g.N : g.K;
+    CUtensorMap ta, tb, tsa, tsb, tc;
+    fp8rl_status e = FP8RL_OK;
+    if ((e = make_tmap(&ta, g.a, wgrad ? g.N : l.R, kr, kr, 128)) != FP8RL_OK) return e;
+    if (op == EXPERT_FWD) e = make_tmap(&tb, g.b, l.E * g.N, g.K, g.K, 128);
+    else if (op == EXPERT_DGRAD) e = make_tmap(&tb, g.b, g.K, l.E * g.N, l.E * g.N, 128);
+    else e = make_tmap(&tb, g.b, g.K, l.R, l.R, 128);
+    if (e != FP8RL_OK) return e;
+    if (wgrad) {
+        if ((e = make_tmap_scales(&tsa, g.sa, l.R / 128, g.N, 128, 1)) != FP8RL_OK) return e;
+        if ((e = make_tmap_scales(&tsb, g.sb, l.R / 128, g.K, 256, 1)) != FP8RL_OK) return e;
+        e = make_tmap_out(&tc, g.c, l.E * g.N, g.K, g.K);
+    } else {
+        if ((e = make_tmap_scales(&tsa, g.sa, kr / 128, l.R, 128, (int)std::min<int64_t>(4, kr / 128))) != FP8RL_OK) return e;
+        tsb = tsa;   // unused
+        e = make_tmap_out(&tc, g.c, l.R, cols, cols);
+    }
+    if (e != FP8RL_OK) return e;
+    ExpertGemmParams p = {};
+    p.start = l.start;
+    p.E = (int)l.E;
+    p.R = (int)l.R;
+    p.rows = (int)g.N;
+    p.cols = (int)cols;
+    p.nkb = (int)(kr / 128);
+    p.b_x = op == EXPERT_DGRAD ? (int)g.N : 0;
+    p.b_y = op == EXPERT_FWD ? (int)g.N : 0;
+    p.sb = g.sb;
+    p.sb_e = (g.N / 128) * (g.K / 128);
+    p.sb_c = op == EXPERT_FWD ? g.K / 128 : 1;
+    p.sb_kb = op == EXPERT_FWD ? 1 : g.K / 128;
+    p.timeout_ns = g_timeout_ns.load();
+    // tiles: at most one more 256-row tile an expert than the rows fill
+    const int64_t n_tiles = (cols + 255) / 256;
+    const int64_t units = wgrad ? l.E * ((g.N + 255) / 256) : l.R / 256 + l.E;
+    if (units > (int64_t(1) << 30) / n_tiles) return FP8RL_ERR_SHAPE;
+    const int clusters = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / 2, units * n_tiles));
+    return cuda_status(launch_gemm_experts(ta, tb, tsa, tsb, tc, p, wgrad, clusters, st));
+}
+
+// The forward product of align 1.
+fp8rl_status run_decode_experts(const ExpertArgs& g, const fp8rl_expert_layout& l, int num_sms, cudaStream_t st) {
+    const int64_t P = l.T * l.k, tiles = g.N / 128, nkb = g.K / 128;
+    const int tokens = expert_decode_tokens(P, l.E);
+    const int64_t units = std::min(l.E, P) + P / tokens;    // sum of ceil(count / tokens) is no more
+    const int splits = expert_decode_splits(units, tiles, nkb, num_sms);
+    if (units * tiles > (int64_t(1) << 30) / splits) return FP8RL_ERR_SHAPE;
+    CUtensorMap tw, tx;
+    fp8rl_status e = make_tmap(&tw, g.b, l.E * g.N, g.K, g.K, 128);
+    if (e != FP8RL_OK) return e;
+    if ((e = make_tmap(&tx, g.a, l.R, g.K, g.K, tokens)) != FP8RL_OK) return e;
+    ExpertDecodeParams p = {};
+    p.start = l.start;
+    p.count = l.count;
+    p.E = (int)l.E;
+    p.nkb = (int)nkb;
+    p.tiles = (int)tiles;
+    p.sx = g.sa;
+    p.R = l.R;
+    p.sw = g.sb;
+    p.y = g.c;
+    p.ldy = g.N;
+    p.timeout_ns = g_timeout_ns.load();
+    return cuda_status(launch_decode_experts(tw, tx, p, tokens, units, splits, st));
+}
+
+fp8rl_status gemm_experts(ExpertOp op, const ExpertArgs& g, const fp8rl_expert_layout* rows, cudaStream_t st) {
+    fp8rl_status e = check_layout(rows, op == EXPERT_FWD && rows && rows->align == 1 ? "bc" : "b");
+    if (e != FP8RL_OK) return e;
+    if ((e = check_expert_weights(g.N, g.K, rows->E)) != FP8RL_OK) return e;
+    if (op != EXPERT_FWD && rows->align != kExpertAlign) return FP8RL_ERR_SHAPE;
+    if (op != EXPERT_WGRAD && rows->T == 0) return FP8RL_OK;
+    if (!g.c || (rows->T > 0 && (!g.a || !g.sa || !g.b || !g.sb))) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(g.a) || !aligned16(g.sa) || !aligned16(g.b) || !aligned16(g.sb) || !aligned16(g.c)) return FP8RL_ERR_ALIGN;
+    int sms = 0;
+    if ((e = current_device(&sms)) != FP8RL_OK) return e;
+    if (rows->T == 0) return cuda_status(cudaMemsetAsync(g.c, 0, (size_t)(rows->E * g.N * g.K) * 2, st));
+    if (rows->align != kExpertAlign) return run_decode_experts(g, *rows, sms, st);
+    return run_gemm_experts(op, g, *rows, sms, st);
+}
+
+}  // namespace
+
+fp8rl_status fp8rl_route_topk(const fp8rl_route_args* a, int64_t T, int64_t E, fp8rl_stream_t stream) {
+    if (!a || T < 0 || E < 1 || a->ld < E || a->k < 1 || a->n_groups < 1 || a->top_groups < 1 || a->top_groups > a->n_groups ||
+        a->group_rank < 1 || a->group_rank > 2 || (a->score != FP8RL_SCORE_SOFTMAX && a->score != FP8RL_SCORE_SIGMOID) ||
+        !(a->scale - a->scale == 0.0f))
+        return FP8RL_ERR_INVALID_ARG;
+    if (E > kMaxExperts || a->n_groups > kMaxGroups || E % a->n_groups != 0 || a->k > kMaxTopK ||
+        a->k > a->top_groups * (E / a->n_groups) || T > kMaxPairs / a->k)
+        return FP8RL_ERR_SHAPE;
+    if (T == 0) return FP8RL_OK;
+    if (!a->logits || !a->weight || !a->index) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned_to(a->logits, a->bf16 ? 2 : 4) || !aligned_to(a->bias, 4) || !aligned_to(a->weight, 4) || !aligned_to(a->index, 4))
+        return FP8RL_ERR_ALIGN;
+    fp8rl_status e = current_device(nullptr);
+    if (e != FP8RL_OK) return e;
+    return cuda_status(launch_route_topk(*a, T, E, stream));
+}
+
+fp8rl_status fp8rl_route_topk_bwd(const fp8rl_route_bwd_args* a, int64_t T, int64_t E, fp8rl_stream_t stream) {
+    if (!a || T < 0 || E < 1 || a->ld < E || a->ldd < E || a->k < 1 ||
+        (a->score != FP8RL_SCORE_SOFTMAX && a->score != FP8RL_SCORE_SIGMOID) || !(a->scale - a->scale == 0.0f))
+        return FP8RL_ERR_INVALID_ARG;
+    if (E > kMaxExperts || a->k > kMaxTopK || T > kMaxPairs / a->k) return FP8RL_ERR_SHAPE;
+    if (T == 0) return FP8RL_OK;
+    if (!a->dweight || !a->logits || !a->index || !a->dlogits) return FP8RL_ERR_INVALID_ARG;
+    const size_t el = a->bf16 ? 2 : 4;
+    if (!aligned_to(a->logits, el) || !aligned_to(a->dlogits, el) || !aligned_to(a->dweight, 4) || !aligned_to(a->index, 4))
+        return FP8RL_ERR_ALIGN;
+    fp8rl_status e = current_device(nullptr);
+    if (e != FP8RL_OK) return e;
+    return cuda_status(launch_route_topk_bwd(*a, T, E, stream));
+}
+
+int64_t fp8rl_expert_rows_capacity(int64_t T, int64_t k, int64_t E, int64_t align) {
+    if (!expert_sizes(T, k, E, align)) return 0;
+    const int64_t P = T * k;
+    return (P + std::min(E, P) * (align - 1)) / align * align;
+}
+
+size_t fp8rl_expert_rows_workspace_bytes(int64_t T, int64_t k, int64_t E) {
+    if (!expert_sizes(T, k, E, 1) || T == 0) return 0;
+    const int nb = expert_rows_blocks(T * k);
+    return nb > 1 ? (size_t)nb * E * sizeof(int32_t) : 0;
+}
+
+fp8rl_status fp8rl_expert_rows(const int32_t* index, int64_t T, int64_t k, int64_t E, int64_t align, int32_t* pos, int32_t* src,
+                               int32_t* start, int32_t* count, void* ws, size_t ws_bytes, fp8rl_stream_t stream) {
+    if (T < 0 || k < 1 || E < 1) return FP8RL_ERR_INVALID_ARG;
+    if (!expert_sizes(T, k, E, align)) return FP8RL_ERR_SHAPE;
+    if (!start || !count || (T > 0 && (!index || !pos || !src))) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned_to(index, 4) || !aligned_to(pos, 4) || !aligned16(src) || !aligned16(start) || !aligned_to(count, 4))
+        return FP8RL_ERR_ALIGN;
+    const size_t need = fp8rl_expert_rows_workspace_bytes(T, k, E);
+    if (need > 0 && (!ws || ws_bytes < need)) return FP8RL_ERR_WORKSPACE;
+    if (need > 0 && !aligned_to(ws, 4)) return FP8RL_ERR_ALIGN;
+    fp8rl_status e = current_device(nullptr);
+    if (e != FP8RL_OK) return e;
+    return cuda_status(launch_expert_rows(index, T * k, (int)E, (int)align, fp8rl_expert_rows_capacity(T, k, E, align), pos, src,
+                                          start, count, reinterpret_cast<int32_t*>(ws), stream));
+}
+
+fp8rl_status fp8rl_expert_gather_quant(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
+                                       const fp8rl_expert_layout* rows, uint8_t* q, float* s, uint8_t* qT, float* sT,
+                                       fp8rl_stream_t stream) {
+    fp8rl_status e = check_layout(rows, "s");
+    if (e != FP8RL_OK) return e;
+    if (K <= 0 || ldx < K || (qT == nullptr) != (sT == nullptr)) return FP8RL_ERR_INVALID_ARG;
+    if (K % 128 != 0 || (qT && rows->align != kExpertAlign)) return FP8RL_ERR_SHAPE;
+    if (rows->T == 0) return FP8RL_OK;
+    if (!x || !q || !s) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(s) || !aligned16(qT) || !aligned16(sT) || (ldx * 2) % 16 != 0 ||
+        !aligned_to(weight, 4))
+        return FP8RL_ERR_ALIGN;
+    int sms = 0;
+    if ((e = current_device(&sms)) != FP8RL_OK) return e;
+    if (qT) return cuda_status(launch_expert_gather_dual(x, ldx, K, weight, *rows, q, s, qT, sT, g_timeout_ns.load(), stream));
+    return cuda_status(launch_expert_gather_rows(x, ldx, K, weight, *rows, q, s, sms, stream));
+}
+
+fp8rl_status fp8rl_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,
+                                  int64_t ldr, const fp8rl_expert_layout* rows, uint16_t* out, int64_t ldo,
+                                  fp8rl_stream_t stream) {
+    fp8rl_status e = check_layout(rows, "p");
+    if (e != FP8RL_OK) return e;
+    if (N <= 0 || ldy < N || ldo < N || (residual && ldr < N)) return FP8RL_ERR_INVALID_ARG;
+    if (N % 8 != 0) return FP8RL_ERR_SHAPE;
+    if (rows->T == 0) return FP8RL_OK;
+    if (!y || !out) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(y) || !aligned16(out) || !aligned16(residual) || (ldy * 2) % 16 != 0 || (ldo * 2) % 16 != 0 ||
+        (residual && (ldr * 2) % 16 != 0) || !aligned_to(weight, 4))
+        return FP8RL_ERR_ALIGN;
+    if ((e = current_device(nullptr)) != FP8RL_OK) return e;
+    return cuda_status(launch_expert_combine(y, ldy, N, weight, residual, ldr, *rows, out, ldo, stream));
+}
+
+fp8rl_status fp8rl_expert_combine_dweight(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t ldy, int64_t N,
+                                          const fp8rl_expert_layout* rows, float* dweight, fp8rl_stream_t stream) {
+    fp8rl_status e = check_layout(rows, "p");
+    if (e != FP8RL_OK) return e;
+    if (N <= 0 || ldd < N || ldy < N) return FP8RL_ERR_INVALID_ARG;
+    if (N % 8 != 0) return FP8RL_ERR_SHAPE;
+    if (rows->T == 0) return FP8RL_OK;
+    if (!dout || !y || !dweight) return FP8RL_ERR_INVALID_ARG;
+    if (!aligned16(dout) || !aligned16(y) || !aligned_to(dweight, 4) || (ldd * 2) % 16 != 0 || (ldy * 2) % 16 != 0)
+        return FP8RL_ERR_ALIGN;
+    if ((e = current_device(nullptr)) != FP8RL_OK) return e;
+    return cuda_status(launch_expert_dweight(dout, ldd, y, ldy, N, *rows, dweight, stream));
+}
+
+fp8rl_status fp8rl_gemm_experts_fwd(const uint8_t* qx, const float* sx, const uint8_t* qw, const float* sw, uint16_t* y,
+                                    int64_t N, int64_t K, const fp8rl_expert_layout* rows, fp8rl_stream_t stream) {
+    return gemm_experts(EXPERT_FWD, ExpertArgs{qx, sx, qw, sw, y, N, K}, rows, stream);
+}
+
+fp8rl_status fp8rl_gemm_experts_dgrad(const uint8_t* qdy, const float* sdy, const uint8_t* qwT, const float* sw, uint16_t* dx,
+                                      int64_t N, int64_t K, const fp8rl_expert_layout* rows, fp8rl_stream_t stream) {
+    return gemm_experts(EXPERT_DGRAD, ExpertArgs{qdy, sdy, qwT, sw, dx, N, K}, rows, stream);
+}
+
+fp8rl_status fp8rl_gemm_experts_wgrad(const uint8_t* qdyT, const float* sdyT, const uint8_t* qxT, const float* sxT, uint16_t* dw,
+                                      int64_t N, int64_t K, const fp8rl_expert_layout* rows, fp8rl_stream_t stream) {
+    return gemm_experts(EXPERT_WGRAD, ExpertArgs{qdyT, sdyT, qxT, sxT, dw, N, K}, rows, stream);
+}
 
 // ---------------------------------------------------------------- diagnostics
 

@@ -1,0 +1,309 @@
+// expert_rows.cu -- between token order and expert order: the stable sort of (token, expert) pairs,
+// the gather of token rows into it with their 1x128 quantization, and the weighted sum back.
+//
+// Row layout (fp8rl_expert_layout): expert e's pairs, in the order of p = t k + j, take rows
+// start[e] .. start[e] + count[e]; start[e + 1] is the next multiple of `align` after them.
+#include <algorithm>
+
+#include "common.cuh"
+#include "experts.h"
+#include "quant_common.cuh"
+
+namespace fp8rl {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kSortWarps = 16;
+constexpr int64_t kSortChunk = 2048;     // pairs of a block of the sort, at least
+constexpr int kSortMaxBlocks = 128;
+
+__device__ __forceinline__ uint4 ldg_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// ---------------------------------------------------------------- the sort
+
+// Histogram of one block's pairs (an index outside [0, E) is no pair).
+__global__ void __launch_bounds__(32 * kSortWarps) k_expert_hist(const int32_t* __restrict__ index, int64_t P, int E,
+                                                                 int64_t chunk, int32_t* __restrict__ hist) {
+    extern __shared__ int32_t s_hist[];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s_hist[e] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min(lo + chunk, P);
+    for (int64_t p = lo + threadIdx.x; p < hi; p += blockDim.x) {
+        const int e = __ldg(index + p);
+        if ((unsigned)e < (unsigned)E) atomicAdd(&s_hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(int64_t)blockIdx.x * E + e] = s_hist[e];
+}
+
+// Places one block's pairs.  Each warp has a contiguous part of them: the warps' counts, summed over
+// the warps and blocks before, give every warp its first row of each expert, and within 32 pairs
+// match_any ranks the pairs of one expert by lane, so the order is that of the pairs.
+// s_n: [kSortWarps][E] counts, then first rows; s_start [E + 1].
+__global__ void __launch_bounds__(32 * kSortWarps) k_expert_place(const int32_t* __restrict__ index, int64_t P, int E,
+                                                                  int64_t chunk, int align, int64_t R,
+                                                                  const int32_t* __restrict__ hist, int32_t* __restrict__ pos,
+                                                                  int32_t* __restrict__ src, int32_t* __restrict__ start,
+                                                                  int32_t* __restrict__ count) {
+    extern __shared__ int32_t s_n[];
+    int32_t* const s_start = s_n + kSortWarps * E;
+    int32_t* const s_count = s_start + E + 1;
+    __shared__ int32_t s_warp[kSortWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nb = gridDim.x, b = blockIdx.x;
+    for (int i = tid; i < kSortWarps * E; i += blockDim.x) s_n[i] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)b * chunk, hi = min(lo + chunk, P);
+    const int64_t part = ((hi - lo + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t wlo = min(lo + warp * part, hi), whi = min(wlo + part, hi);
+    int32_t* const mine = s_n + warp * E;
+    for (int64_t p = wlo + lane; p < whi; p += 32) {
+        const int e = __ldg(index + p);
+        if ((unsigned)e < (unsigned)E) atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    // all pairs of expert e, those of the blocks before, and from the padded counts the starts
+    int32_t carry = 0;
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + tid;
+        int32_t all = 0, before = 0;
+        if (e < E) {
+            if (nb > 1) {
+                #pragma unroll 8
+                for (int i = 0; i < nb; ++i) {
+                    const int32_t h = __ldg(hist + (int64_t)i * E + e);
+                    all += h;
+                    before += i < b ? h : 0;
+                }
+            } else {
+                for (int w = 0; w < kSortWarps; ++w) all += s_n[w * E + e];
+            }
+        }
+        const int32_t padded = (all + align - 1) / align * align;
+        int32_t scan = padded;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(kFull, scan, o);
+            if (lane >= o) scan += v;
+        }
+        if (lane == 31) s_warp[warp] = scan;
+        __syncthreads();
+        int32_t off = carry, total = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            off += w < warp ? s_warp[w] : 0;
+            total += s_warp[w];
+        }
+        if (e < E) {
+            const int32_t first = off + scan - padded;
+            s_start[e] = first;
+            s_count[e] = all;
+            int32_t at = first + before;
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int32_t n = s_n[w * E + e];
+                s_n[w * E + e] = at;
+                at += n;
+            }
+        }
+        carry += total;
+        __syncthreads();
+    }
+    if (tid == 0) s_start[E] = carry;
+    __syncthreads();
+    if (b == 0) {
+        for (int e = tid; e <= E; e += blockDim.x) start[e] = s_start[e];
+        for (int e = tid; e < E; e += blockDim.x) count[e] = s_count[e];
+    }
+    for (int64_t p0 = wlo; p0 < whi; p0 += 32) {
+        const int64_t p = p0 + lane;
+        const int raw = p < whi ? __ldg(index + p) : -1;
+        const int e = (unsigned)raw < (unsigned)E ? raw : -1;
+        const uint32_t same = __match_any_sync(kFull, e);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        int32_t row = -1;
+        if (e >= 0) row = mine[e] + rank;
+        __syncwarp();
+        if (e >= 0 && rank == 0) mine[e] += __popc(same);
+        __syncwarp();
+        if (p < whi) pos[p] = row;
+        if (row >= 0) src[row] = (int32_t)p;
+    }
+    // rows of no pair: the experts' padding (a warp an expert) and the rest of the buffer
+    if (align > 1)
+        for (int e = b * kSortWarps + warp; e < E; e += nb * kSortWarps)
+            for (int r = s_start[e] + s_count[e] + lane; r < s_start[e + 1]; r += 32) src[r] = -1;
+    for (int64_t r = (int64_t)s_start[E] + (int64_t)b * blockDim.x + tid; r < R; r += (int64_t)nb * blockDim.x) src[r] = -1;
+}
+
+// ---------------------------------------------------------------- gather + quantize
+
+// Rows in expert order, 1x128: 16 threads a group of 128 as in k_quant_1x128, the groups numbered
+// block-major so that neighbouring groups' scales are stored together.  A weighted row is rounded to
+// BF16 before it is quantized, as the gradient between operators is.  Rows without a pair give zeros.
+__global__ void __launch_bounds__(256) k_expert_gather_rows(const uint16_t* __restrict__ x, int64_t ldx, int64_t K,
+                                                            const float* __restrict__ weight, const int32_t* __restrict__ src,
+                                                            int64_t T, int k, int64_t R, uint8_t* __restrict__ q,
+                                                            float* __restrict__ s) {
+    const int sub = threadIdx.x & 15;
+    const int half = (threadIdx.x >> 4) & 1;
+    const int warp = threadIdx.x >> 5;
+    const int64_t ngroups = R * (K / 128);
+    const int64_t step = (int64_t)gridDim.x * 16;
+    for (int64_t base = (int64_t)blockIdx.x * 16 + warp * 2; base < ngroups; base += step) {
+        const int64_t g = base + half;
+        const bool valid = g < ngroups;
+        const int64_t kb = valid ? g / R : 0;
+        const int64_t r = valid ? g - kb * R : 0;
+        const int p = __ldg(src + r);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (valid && p >= 0 && p < T * k) {
+            v = ldg_v4(x + (int64_t)(p / k) * ldx + kb * 128 + sub * 8);
+            if (weight) {
+                const float w = __ldg(weight + p);
+                uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+                #pragma unroll
+                for (int j = 0; j < 4; ++j) u[j] = pack_bf16x2(bf16_lo(u[j]) * w, bf16_hi(u[j]) * w);
+            }
+        }
+        uint32_t mx = absmax2(absmax2(absmax2(absmax2(0u, v.x), v.y), v.z), v.w);
+        mx = max(mx & 0xFFFFu, mx >> 16);
+        #pragma unroll
+        for (int off = 8; off >= 1; off >>= 1) mx = max(mx, __shfl_xor_sync(kFull, mx, off));
+        const GroupScale gs = make_scale(bf16_bits_amax_to_f32(mx));
+        const uint32_t c0 = encode_pair(bf16_lo(v.x), bf16_hi(v.x), gs);
+        const uint32_t c1 = encode_pair(bf16_lo(v.y), bf16_hi(v.y), gs);
+        const uint32_t c2 = encode_pair(bf16_lo(v.z), bf16_hi(v.z), gs);
+        const uint32_t c3 = encode_pair(bf16_lo(v.w), bf16_hi(v.w), gs);
+        if (valid) {
+            *reinterpret_cast<uint2*>(q + r * K + kb * 128 + sub * 8) = make_uint2(c0 | (c1 << 16), c2 | (c3 << 16));
+            if (sub == 0) s[kb * R + r] = gs.s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- combine
+
+// out[t] = residual[t] + sum_j weight[t, j] y[pos[t, j]] in FP32 in the order of j: a thread has 8
+// columns of one token.  Pairs without a row (pos outside [0, R)) add nothing.
+__global__ void __launch_bounds__(256) k_expert_combine(const uint16_t* __restrict__ y, int64_t ldy, int64_t N,
+                                                        const float* __restrict__ weight, const uint16_t* __restrict__ residual,
+                                                        int64_t ldr, const int32_t* __restrict__ pos, int64_t T, int k, int64_t R,
+                                                        uint16_t* __restrict__ out, int64_t ldo) {
+    const int64_t per = N / 8;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < T * per; i += step) {
+        const int64_t t = i / per, c = (i - t * per) * 8;
+        float acc[8];
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+        #pragma unroll 4
+        for (int j = 0; j < k; ++j) {
+            const int r = __ldg(pos + t * k + j);
+            if ((unsigned)r >= (unsigned)R) continue;
+            const float w = weight ? __ldg(weight + t * k + j) : 1.0f;
+            const uint4 v = ldg_v4(y + (int64_t)r * ldy + c);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            #pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                acc[2 * h] = fmaf(w, bf16_lo(u[h]), acc[2 * h]);
+                acc[2 * h + 1] = fmaf(w, bf16_hi(u[h]), acc[2 * h + 1]);
+            }
+        }
+        if (residual) {
+            const uint4 v = ldg_v4(residual + t * ldr + c);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            #pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                acc[2 * h] += bf16_lo(u[h]);
+                acc[2 * h + 1] += bf16_hi(u[h]);
+            }
+        }
+        uint4 o;
+        o.x = pack_bf16x2(acc[0], acc[1]);
+        o.y = pack_bf16x2(acc[2], acc[3]);
+        o.z = pack_bf16x2(acc[4], acc[5]);
+        o.w = pack_bf16x2(acc[6], acc[7]);
+        *reinterpret_cast<uint4*>(out + t * ldo + c) = o;
+    }
+}
+
+// dweight[t, j] = <dout[t], y[pos[t, j]]>, a warp a pair; 0 for a pair without a row.
+__global__ void __launch_bounds__(256) k_expert_dweight(const uint16_t* __restrict__ dout, int64_t ldd,
+                                                        const uint16_t* __restrict__ y, int64_t ldy, int64_t N,
+                                                        const int32_t* __restrict__ pos, int64_t P, int k, int64_t R,
+                                                        float* __restrict__ dweight) {
+    const int lane = threadIdx.x & 31;
+    const int64_t p = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (p >= P) return;
+    const int r = __ldg(pos + p);
+    float acc = 0.0f;
+    if ((unsigned)r < (unsigned)R) {
+        const uint16_t* a = dout + (p / k) * ldd;
+        const uint16_t* b = y + (int64_t)r * ldy;
+        #pragma unroll 4
+        for (int64_t c = lane * 8; c < N; c += 256) {
+            const uint4 va = ldg_v4(a + c), vb = ldg_v4(b + c);
+            const uint32_t ua[4] = {va.x, va.y, va.z, va.w}, ub[4] = {vb.x, vb.y, vb.z, vb.w};
+            #pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                acc = fmaf(bf16_lo(ua[h]), bf16_lo(ub[h]), acc);
+                acc = fmaf(bf16_hi(ua[h]), bf16_hi(ub[h]), acc);
+            }
+        }
+    }
+    #pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
+    if (lane == 0) dweight[p] = acc;
+}
+
+}  // namespace
+
+int expert_rows_blocks(int64_t P) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kSortMaxBlocks, (P + kSortChunk - 1) / kSortChunk));
+}
+
+cudaError_t launch_expert_rows(const int32_t* index, int64_t P, int E, int align, int64_t R, int32_t* pos, int32_t* src,
+                               int32_t* start, int32_t* count, int32_t* hist, cudaStream_t st) {
+    const int nb = expert_rows_blocks(P);
+    const int64_t chunk = (P + nb - 1) / nb;
+    if (nb > 1) {
+        k_expert_hist<<<nb, 32 * kSortWarps, (size_t)E * 4, st>>>(index, P, E, chunk, hist);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const size_t smem = ((size_t)kSortWarps * E + 2 * E + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(((size_t)kSortWarps + 2) * kMaxExperts * 4 + 4));
+    if (e != cudaSuccess) return e;
+    k_expert_place<<<nb, 32 * kSortWarps, smem, st>>>(index, P, E, chunk, align, R, hist, pos, src, start, count);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_gather_rows(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
+                                      const fp8rl_expert_layout& l, uint8_t* q, float* s, int num_sms, cudaStream_t st) {
+    const int64_t ngroups = l.R * (K / 128);
+    const int64_t blocks = std::min<int64_t>((ngroups + 15) / 16, (int64_t)num_sms * 16);
+    k_expert_gather_rows<<<(unsigned)blocks, 256, 0, st>>>(x, ldx, K, weight, l.src, l.T, (int)l.k, l.R, q, s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,
+                                  int64_t ldr, const fp8rl_expert_layout& l, uint16_t* out, int64_t ldo, cudaStream_t st) {
+    const int64_t n = l.T * (N / 8);
+    const int64_t blocks = std::min<int64_t>((n + 255) / 256, 1 << 20);
+    k_expert_combine<<<(unsigned)blocks, 256, 0, st>>>(y, ldy, N, weight, residual, ldr, l.pos, l.T, (int)l.k, l.R, out, ldo);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_dweight(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t ldy, int64_t N,
+                                  const fp8rl_expert_layout& l, float* dweight, cudaStream_t st) {
+    const int64_t P = l.T * l.k;
+    k_expert_dweight<<<(unsigned)((P + 7) / 8), 256, 0, st>>>(dout, ldd, y, ldy, N, l.pos, P, (int)l.k, l.R, dweight);
+    return cudaGetLastError();
+}
+
+}  // namespace fp8rl

@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "block.h"
+#include "experts.h"
 #include "gemm.h"
 #include "quant_common.cuh"
 
@@ -95,8 +96,10 @@ __global__ void __launch_bounds__(256) k_quant_1x128(const uint16_t* __restrict_
 // PRO_SILU_BWD from that checkpoint: 989 us at 16384 x 27648 dual (0.56; from BF16 1061 us).  Both
 // use 55 to 58% of the issue slots: three or four encodes and a sigmoid per element, each a chain of
 // dependent instructions, with 16 warps an SM to fill the gaps.
+// PRO_GATHER quantizes rows of x in the order of an index (an expert's rows together), each times a
+// weight where one is given and rounded to BF16; rows without a source are zeros.
 enum Prologue : int { PRO_COPY = 0, PRO_SILU = 1, PRO_RMSNORM = 2, PRO_RMSNORM_G = 3, PRO_SILU_BWD = 5,
-                      PRO_DEQUANT = 6, PRO_SILU_BWD_CK = 7, PRO_SILU_CK = 8 };
+                      PRO_DEQUANT = 6, PRO_SILU_BWD_CK = 7, PRO_SILU_CK = 8, PRO_GATHER = 9 };
 
 struct PanelArgs {
     const uint16_t* x;      // COPY / RMSNORM: x[M][ldx];  SILU: gu[M][ldx], ldx = 2*K;
@@ -116,6 +119,12 @@ struct PanelArgs {
     float* sT;              // scales sT[M/128][K]
     int tiles_per_cta;      // RMSNorm: 128-column sub-tiles handled by one CTA of a panel's cluster
     uint64_t timeout_ns;    // bound of every wait on a TMA copy
+    // GATHER: x[x_rows][ldx]; row m of the result comes from pair p = src[m], row p / k of x, and is
+    // multiplied by weight[p] (nullable); zeros where p is outside [0, k x_rows)
+    const int32_t* src;
+    const float* weight;
+    int64_t x_rows;
+    int k;
 };
 
 // Accurate sum of squares: binary32 pairs (hi, lo) updated with the exact two-sum, so
@@ -485,6 +494,8 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         }
     };
 
+    // who requests tiles: thread 0, or all of warp 0 with four gathered rows a lane
+    const bool issuer = PRO == PRO_GATHER ? warp == 0 : tid == 0;
     if (tid == 0) {
         for (int st = 0; st < STAGES; ++st) mbar_init(smem_u32(&full_bar[st]), 1);
         abort_flag = 0;
@@ -502,6 +513,16 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         const int64_t k0 = tt * 128, m0 = pnl * 128;
         const uint32_t bar = smem_u32(&full_bar[st]);
         uint8_t* dst = stages + st * PS::STAGE_BYTES;
+        if (PRO == PRO_GATHER) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, PS::STAGE_BYTES);
+            __syncwarp();
+            const int4 p = __ldg(reinterpret_cast<const int4*>(a.src + m0) + lane);
+            const int64_t pairs = a.x_rows * a.k;
+            // a row without a source is read from row 0 and masked after the copy
+            auto row = [&](int v) { return v >= 0 && v < pairs ? v / a.k : 0; };
+            tma_gather4(smem_u32(dst) + 1024u * lane, &tmx, bar, (int)k0, make_int4(row(p.x), row(p.y), row(p.z), row(p.w)));
+            return;
+        }
         if (part != 2) mbar_arrive_expect_tx(bar, PS::STAGE_BYTES);
         if (PRO == PRO_DEQUANT) {
             // the code tile and the 128 row scales of its column block (one bulk copy:
@@ -528,7 +549,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         }
     };
     int issued = 0;
-    if (tid == 0)
+    if (issuer)
         for (; issued < STAGES && issued < total; ++issued) issue(issued);
     // every thread waits for item `it`; the decision to stop is made block-wide
     auto wait_item = [&](int it) -> bool {
@@ -605,11 +626,24 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         const int64_t m = pnl * 128 + R0 + (cl & 7);
         return m < a.M ? __ldg(a.xs + (tt + (cl < 8 ? 0 : ntiles / 2)) * a.M + m) : 0.0f;
     };
+    // GATHER: lane cl holds the factor of row R0 + (cl & 7) of its half, likewise, and whether
+    // the row has a source
+    auto row_factor = [&](int it) {
+        int64_t pnl, tt;
+        tile_at(it, pnl, tt);
+        const int p = __ldg(a.src + pnl * 128 + R0 + (cl & 7));
+        const bool has = p >= 0 && p < a.x_rows * a.k;
+        return make_float2(!has ? 0.0f : a.weight ? __ldg(a.weight + p) : 1.0f, has ? 1.0f : 0.0f);
+    };
     float ck_next = 0.0f;
+    float2 rf_next = make_float2(0.0f, 0.0f);
     if (PRO == PRO_SILU_BWD_CK && total > 0) ck_next = ckpt_scale(0);
+    if (PRO == PRO_GATHER && total > 0) rf_next = row_factor(0);
     for (; ok && item < total; ++item) {
         const float ck_scale = ck_next;
+        const float2 rf = rf_next;
         if (PRO == PRO_SILU_BWD_CK && item + 1 < total) ck_next = ckpt_scale(item + 1);
+        if (PRO == PRO_GATHER && item + 1 < total) rf_next = row_factor(item + 1);
         ok = wait_item(item);
         if (!ok) break;
         int64_t panel, t;
@@ -660,7 +694,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             // double the registers and halve the CTAs per SM
             auto xrow = [&](int i, int j) { return make_float2(bf16_lo(w[i][j]), bf16_hi(w[i][j])); };
             __syncthreads();                                  // stage consumed, column maxima published
-            if (tid == 0 && issued < total) {
+            if (issuer && issued < total) {
                 if (refill == 1) issue(issued++);
                 else if (refill == 2) issue(issued, 1);
             }
@@ -881,7 +915,19 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             #pragma unroll
             for (int i = 0; i < 8; ++i)   // rows past M (TMA zero fill) are never stored
                 rg[i] = (PRO == PRO_RMSNORM_G && m0 + R0 + i < a.M) ? __ldg(a.rstd_out + m0 + R0 + i) : 0.0f;
-            rows_from_smem<PRO>(stage, a, t * 128, R0, C0, s_rstd, rg, w);
+            rows_from_smem<PRO == PRO_GATHER ? PRO_COPY : PRO>(stage, a, t * 128, R0, C0, s_rstd, rg, w);
+            if (PRO == PRO_GATHER) {
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = __shfl_sync(0xffffffffu, rf.x, (lane & 16) | i);
+                    const bool has = __shfl_sync(0xffffffffu, rf.y, (lane & 16) | i) != 0.0f;
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (a.weight) w[i][j] = pack_bf16x2(bf16_lo(w[i][j]) * f, bf16_hi(w[i][j]) * f);
+                        if (!has) w[i][j] = 0u;
+                    }
+                }
+            }
             // this tile's qT staging buffer (two, alternating: the next tile's barrier orders
             // this tile's reads before the writes of the tile after)
             quantize_tile(w, t, smem_u32(stages + PS::COLQ_OFF) + (uint32_t)(item & 1) * (128u * 128u), 1);
@@ -1143,13 +1189,14 @@ cudaError_t launch_quant_1x128(const uint16_t* x, int64_t M, int64_t K, int64_t 
     return cudaGetLastError();
 }
 
-// 2-D tensor map of a BF16 matrix [rows][cols] (row stride ld elements), 128x128 boxes.
-static cudaError_t tmap_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
+// 2-D tensor map of a BF16 matrix [rows][cols] (row stride ld elements), box_rows x 128 boxes.
+static cudaError_t tmap_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                             unsigned box_rows = 128) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return cudaErrorNotSupported;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {128u, 128u};
+    cuuint32_t box[2] = {128u, box_rows};
     cuuint32_t es[2] = {1u, 1u};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -1175,7 +1222,9 @@ template <int PRO, bool ROW_OUT, bool COL_OUT>
 static cudaError_t launch_panel_t(const PanelArgs& a, int64_t in_cols, int cluster, cudaStream_t st) {
     CUtensorMap tm, tm2;
     constexpr bool pair = PRO == PRO_SILU_BWD || PRO == PRO_SILU_BWD_CK;
-    cudaError_t e = PRO == PRO_DEQUANT || PRO == PRO_SILU_BWD_CK ? tmap_u8(&tm, a.x, a.M, in_cols) : tmap_bf16(&tm, a.x, a.M, in_cols, a.ldx);
+    cudaError_t e = PRO == PRO_DEQUANT || PRO == PRO_SILU_BWD_CK ? tmap_u8(&tm, a.x, a.M, in_cols)
+                    : PRO == PRO_GATHER ? tmap_bf16(&tm, a.x, a.x_rows, in_cols, a.ldx, 1)
+                                        : tmap_bf16(&tm, a.x, a.M, in_cols, a.ldx);
     if (e != cudaSuccess) return e;
     if (pair) {
         e = tmap_bf16(&tm2, a.x2, a.M, a.K / 2, a.K / 2);
@@ -1230,6 +1279,17 @@ cudaError_t launch_quant_dual(const uint16_t* x, int64_t M, int64_t K, int64_t l
     a.timeout_ns = timeout_ns;
     if (q) return launch_panel_t<PRO_COPY, true, true>(a, K, 0, st);
     return launch_panel_t<PRO_COPY, false, true>(a, K, 0, st);
+}
+
+// rows of x in expert order, each times its pair's weight, quantized 1x128 and 128x1
+cudaError_t launch_expert_gather_dual(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
+                                      const fp8rl_expert_layout& l, uint8_t* q, float* s, uint8_t* qT, float* sT,
+                                      uint64_t timeout_ns, cudaStream_t st) {
+    PanelArgs a = {};
+    a.x = x; a.ldx = ldx; a.M = l.R; a.K = K; a.q = q; a.s = s; a.qT = qT; a.sT = sT;
+    a.src = l.src; a.weight = weight; a.x_rows = l.T; a.k = (int)l.k;
+    a.timeout_ns = timeout_ns;
+    return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
 }
 
 cudaError_t launch_silu_mul_quant(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s,

@@ -676,3 +676,248 @@ def matvec_nvfp4(x: torch.Tensor, qw: torch.Tensor, sfw: torch.Tensor, gw: torch
     check(lib().fp8rl_matvec_nvfp4(_ptr(x), M, K, ldx, _ptr(qw), _ptr(sfw), _ptr(gw), N, _ptr(y), ldy,
                                    int(splits), _stream(dev)), "fp8rl_matvec_nvfp4")
     return y
+
+
+# ------------------------------------------------------------------ expert layers
+
+class Route(NamedTuple):
+    """What route_topk returns: a token's experts, best first (-1: none), and their weights."""
+    weight: torch.Tensor                   # f32 [T,k]
+    index: torch.Tensor                    # i32 [T,k]
+
+
+class ExpertRows(NamedTuple):
+    """(token, expert) pairs in expert order (expert_rows).  Expert e has the rows start[e] ..
+    start[e] + count[e]; start[e + 1] is the next multiple of align after them."""
+    pos: torch.Tensor                      # i32 [T,k] row of each pair, -1 for none
+    src: torch.Tensor                      # i32 [R] pair t k + j of each row, -1 for none
+    start: torch.Tensor                    # i32 [E+1]
+    count: torch.Tensor                    # i32 [E]
+    align: int                             # 128 (training, prefill) or 1 (rollout)
+
+
+_SCORES = {"softmax": _abi.FP8RL_SCORE_SOFTMAX, "sigmoid": _abi.FP8RL_SCORE_SIGMOID}
+
+
+def _logits(t: torch.Tensor, name: str, score: str) -> int:
+    """Checks router logits (f32 or bf16 rows) and the score's name; returns the row stride."""
+    _matrix(t, name)
+    if t.dtype is not torch.float32:
+        _require(t, torch.bfloat16, name)
+    elif not t.is_cuda:
+        _require(t, torch.float32, name)
+    if score not in _SCORES:
+        raise ValueError(f"score: expected 'softmax' or 'sigmoid', got {score!r}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _table(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    if t.dtype is not dtype or t.device != device or not t.is_cuda:
+        _require(t, dtype, name, device)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _contig(t, name)
+
+
+def route_topk(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+               n_groups: int = 1, top_groups: int = 1, group_rank: Optional[int] = None, renormalize: bool = True,
+               scale: float = 1.0) -> Route:
+    """The k experts of each token and their weights from logits f32 or bf16 [T,E].
+
+    The score is the softmax or the sigmoid of the logits; the largest score + bias (f32 [E]) are
+    chosen, the lowest index first among equals, within the `top_groups` of `n_groups` equal groups
+    whose sums of the `group_rank` (1 or 2; by default 2 with a bias, else 1) best are largest.  The
+    weights are the scores, divided by their sum with `renormalize`, times `scale`.  Experts whose
+    logit is -inf are not chosen; a row without k others ends in index -1, weight 0."""
+    ld = _logits(logits, "logits", score)
+    (T, E), dev = logits.shape, logits.device
+    _vector(bias, "bias", torch.float32, E, dev)
+    if group_rank is None:
+        group_rank = 1 if bias is None else 2
+    weight = torch.empty((T, max(int(k), 0)), dtype=torch.float32, device=dev)
+    index = torch.empty((T, max(int(k), 0)), dtype=torch.int32, device=dev)
+    args = _abi.RouteArgs(logits.data_ptr(), ld, logits.dtype is torch.bfloat16, _SCORES[score], _ptr(bias), int(k),
+                          int(n_groups), int(top_groups), int(group_rank), bool(renormalize), float(scale),
+                          weight.data_ptr(), index.data_ptr())
+    check(lib().fp8rl_route_topk(ctypes.byref(args), T, E, _stream(dev)), "fp8rl_route_topk")
+    return Route(weight, index)
+
+
+def route_topk_bwd(dweight: torch.Tensor, logits: torch.Tensor, index: torch.Tensor, *, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """The gradient of route_topk's logits [T,E] (of their type) from dweight f32 [T,k] and the
+    index that it returned."""
+    ld = _logits(logits, "logits", score)
+    (T, E), dev = logits.shape, logits.device
+    _matrix(index, "index")
+    k = index.shape[1]
+    _table(index, "index", torch.int32, (T, k), dev)
+    _table(dweight, "dweight", torch.float32, (T, k), dev)
+    d = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    args = _abi.RouteBwdArgs(dweight.data_ptr(), logits.data_ptr(), ld, logits.dtype is torch.bfloat16, _SCORES[score],
+                             index.data_ptr(), k, bool(renormalize), float(scale), d.data_ptr(), E)
+    check(lib().fp8rl_route_topk_bwd(ctypes.byref(args), T, E, _stream(dev)), "fp8rl_route_topk_bwd")
+    return d
+
+
+def expert_rows(index: torch.Tensor, n_experts: int, align: int = 128) -> ExpertRows:
+    """The pairs of index i32 [T,k] (route_topk's) sorted by expert, in the order of the tokens.
+    An index outside [0, n_experts) is a pair of no expert.  align 128: every expert's rows start at
+    a multiple of 128, as training (and a large prefill) needs; align 1: no padding, for rollout."""
+    _matrix(index, "index")
+    _require(index, torch.int32, "index")
+    _contig(index, "index")
+    (T, k), E, dev = index.shape, int(n_experts), index.device
+    L = lib()
+    R = int(L.fp8rl_expert_rows_capacity(T, k, E, int(align)))
+    # one allocation: src and start 16-byte aligned, then count and pos
+    at, n = [0], E if E > 0 else 0
+    for size in (R, n + 1, n):
+        at.append(at[-1] + (size + 3) // 4 * 4)
+    buf = torch.empty(at[3] + T * k, dtype=torch.int32, device=dev)
+    src, start, count = buf[:R], buf[at[1]:at[1] + n + 1], buf[at[2]:at[2] + n]
+    pos = buf[at[3]:].view(T, k)
+    need = int(L.fp8rl_expert_rows_workspace_bytes(T, k, E))
+    # a buffer of this call's own: calls may run on several streams
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    check(L.fp8rl_expert_rows(_ptr(index), T, k, E, int(align), _ptr(pos), _ptr(src), _ptr(start), _ptr(count), _ptr(ws),
+                              need, _stream(dev)), "fp8rl_expert_rows")
+    return ExpertRows(pos, src, start, count, int(align))
+
+
+def _layout(rows: ExpertRows, dev) -> "_abi.ExpertLayout":
+    """Checks the arrays of an expert order on `dev` and packs them for the C calls."""
+    pos, src, start, count, align = rows
+    _matrix(pos, "rows.pos")
+    (T, k), R, E = pos.shape, src.numel(), count.numel()
+    _table(pos, "rows.pos", torch.int32, (T, k), dev)
+    _vector(src, "rows.src", torch.int32, R, dev)
+    _vector(start, "rows.start", torch.int32, E + 1, dev)
+    _vector(count, "rows.count", torch.int32, E, dev)
+    return _abi.ExpertLayout(pos.data_ptr(), src.data_ptr(), start.data_ptr(), count.data_ptr(), T, k, E, R, int(align))
+
+
+def expert_gather_quant(x: torch.Tensor, rows: ExpertRows, weight: Optional[torch.Tensor] = None, dual: bool = False):
+    """Rows of x bf16 [T,K] in expert order, times the pairs' weight f32 [T,k] where it is given,
+    quantized: (q u8 [R,K], s f32 [K/128,R], qT [K,R] or None, sT [R/128,K] or None).  Rows of no
+    pair are zeros.  `dual` needs align 128."""
+    _matrix(x, "x")
+    _require(x, torch.bfloat16, "x")
+    dev = x.device
+    l = _layout(rows, dev)
+    K = x.shape[1]
+    ldx = _rows(x, "x", (l.T, K), dev)
+    if weight is not None:
+        _table(weight, "weight", torch.float32, (l.T, l.k), dev)
+    q, s = _codes(l.R, K, dev)
+    qT, sT = _codes(K, l.R, dev) if dual else (None, None)
+    check(lib().fp8rl_expert_gather_quant(_ptr(x), ldx, K, _ptr(weight), ctypes.byref(l), _ptr(q), _ptr(s), _ptr(qT),
+                                          _ptr(sT), _stream(dev)), "fp8rl_expert_gather_quant")
+    return q, s, qT, sT
+
+
+def expert_combine(y: torch.Tensor, rows: ExpertRows, weight: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = residual[t] + sum_j weight[t,j] y[pos[t,j]], bf16 [T,N] from y bf16 [R,N] in expert
+    order; without weight (1 each) it is the backward of expert_gather_quant's gather."""
+    _matrix(y, "y")
+    _require(y, torch.bfloat16, "y")
+    dev = y.device
+    l = _layout(rows, dev)
+    N = y.shape[1]
+    ldy = _rows(y, "y", (l.R, N), dev)
+    if weight is not None:
+        _table(weight, "weight", torch.float32, (l.T, l.k), dev)
+    ldr = _rows(residual, "residual", (l.T, N), dev) if residual is not None else 0
+    o = out if out is not None else torch.empty((l.T, N), dtype=torch.bfloat16, device=dev)
+    ldo = _rows(o, "out", (l.T, N), dev)
+    check(lib().fp8rl_expert_combine(_ptr(y), ldy, N, _ptr(weight), _ptr(residual), ldr, ctypes.byref(l), _ptr(o), ldo,
+                                     _stream(dev)), "fp8rl_expert_combine")
+    return o
+
+
+def expert_combine_bwd(dout: torch.Tensor, y: torch.Tensor, rows: ExpertRows, weight: torch.Tensor, dual: bool = True):
+    """Gradients of expert_combine from dout bf16 [T,N]: that of y in expert order, quantized
+    (q [R,N], s [N/128,R], qT [N,R] or None, sT [R/128,N] or None), and dweight f32 [T,k]."""
+    _matrix(y, "y")
+    _require(y, torch.bfloat16, "y")
+    dev = y.device
+    l = _layout(rows, dev)
+    N = y.shape[1]
+    ldy, ldd = _rows(y, "y", (l.R, N), dev), _rows(dout, "dout", (l.T, N), dev)
+    if weight is None:
+        raise ValueError("weight: needed")
+    dweight = torch.empty((l.T, l.k), dtype=torch.float32, device=dev)
+    q = expert_gather_quant(dout, rows, weight, dual=dual)
+    check(lib().fp8rl_expert_combine_dweight(_ptr(dout), ldd, _ptr(y), ldy, N, ctypes.byref(l), _ptr(dweight),
+                                             _stream(dev)), "fp8rl_expert_combine_dweight")
+    return (*q, dweight)
+
+
+def _expert_weights(q, s, shape, N: int, K: int, E: int, dev) -> None:
+    _table(q, "codes W", torch.uint8, shape, dev)
+    _table(s, "scales W", torch.float32, (E * N // 128, K // 128), dev)
+
+
+def _divided(n: int, E: int, name: str) -> int:
+    if n % E != 0:
+        raise ValueError(f"{name}: {n} rows do not divide among {E} experts")
+    return n // E
+
+
+def gemm_experts_fwd(qx, sx, qw, sw, rows: ExpertRows, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[r] = X[r] W_e^T for the rows r of each expert e: qx [R,K], sx [K/128,R] (expert_gather_quant),
+    qw [E N,K], sw [E N/128,K/128] (quantize_128x128 of the experts' weights one below the other)
+    -> y bf16 [R,N].  Rows behind the last expert's are left as they were."""
+    for t, n in ((qx, "qx"), (qw, "codes W")):
+        _matrix(t, n)
+    _require(qx, torch.uint8, "qx")
+    dev = qx.device
+    l = _layout(rows, dev)
+    K, N = qx.shape[1], _divided(qw.shape[0], l.E, "codes W")
+    _table(qx, "qx", torch.uint8, (l.R, K), dev)
+    _table(sx, "sx", torch.float32, (K // 128, l.R), dev)
+    _expert_weights(qw, sw, (l.E * N, K), N, K, l.E, dev)
+    y = _out(out, (l.R, N), dev)
+    check(lib().fp8rl_gemm_experts_fwd(_ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(y), N, K, ctypes.byref(l), _stream(dev)),
+          "fp8rl_gemm_experts_fwd")
+    return y
+
+
+def gemm_experts_dgrad(qdy, sdy, qwT, sw, rows: ExpertRows, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX[r] = dY[r] W_e: qdy [R,N], sdy [N/128,R], qwT [K,E N] and sw (quantize_128x128) -> dx bf16
+    [R,K].  align 128; rows behind the last expert's are left as they were."""
+    for t, n in ((qdy, "qdy"), (qwT, "codes W")):
+        _matrix(t, n)
+    _require(qdy, torch.uint8, "qdy")
+    dev = qdy.device
+    l = _layout(rows, dev)
+    N, K = qdy.shape[1], qwT.shape[0]
+    _table(qdy, "qdy", torch.uint8, (l.R, N), dev)
+    _table(sdy, "sdy", torch.float32, (N // 128, l.R), dev)
+    _expert_weights(qwT, sw, (K, l.E * N), N, K, l.E, dev)
+    dx = _out(out, (l.R, K), dev)
+    check(lib().fp8rl_gemm_experts_dgrad(_ptr(qdy), _ptr(sdy), _ptr(qwT), _ptr(sw), _ptr(dx), N, K, ctypes.byref(l),
+                                         _stream(dev)), "fp8rl_gemm_experts_dgrad")
+    return dx
+
+
+def gemm_experts_wgrad(qdyT, sdyT, qxT, sxT, rows: ExpertRows, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW_e = the sum over expert e's rows r of dY[r]^T X[r]: qdyT [N,R], sdyT [R/128,N], qxT [K,R],
+    sxT [R/128,K] -> dw bf16 [E,N,K], zeros for an expert without rows.  align 128."""
+    for t, n in ((qdyT, "qdyT"), (qxT, "qxT")):
+        _matrix(t, n)
+    _require(qdyT, torch.uint8, "qdyT")
+    dev = qdyT.device
+    l = _layout(rows, dev)
+    N, K = qdyT.shape[0], qxT.shape[0]
+    for q, s, c, n in ((qdyT, sdyT, N, "dyT"), (qxT, sxT, K, "xT")):
+        _table(q, f"q{n}", torch.uint8, (c, l.R), dev)
+        _table(s, f"s{n}", torch.float32, (l.R // 128, c), dev)
+    dw = _out(out, (l.E, N, K), dev)
+    check(lib().fp8rl_gemm_experts_wgrad(_ptr(qdyT), _ptr(sdyT), _ptr(qxT), _ptr(sxT), _ptr(dw), N, K, ctypes.byref(l),
+                                         _stream(dev)), "fp8rl_gemm_experts_wgrad")
+    return dw

@@ -502,6 +502,144 @@ FP8RL_API fp8rl_status fp8rl_matvec_nvfp4(const uint16_t* x, int64_t M, int64_t 
                                           fp8rl_stream_t stream);
 
 /* ----------------------------------------------------------------------------------------
+ * Expert layers: a router picks k of E experts for every token, the tokens' rows are brought
+ * into expert order, every expert's rows are multiplied with its own weights by the scheme's
+ * products, and the results are added up again per token.  The scheme's pages have dense layers
+ * only; the quantization and numerics here are the same.
+ *
+ * Expert weights are one matrix W [E N][K], expert e's rows e N .. (e + 1) N, quantized by
+ * fp8rl_quantize_128x128 as it stands: codes qw [E N][K], scales sw [E N / 128][K / 128] and the
+ * transposed codes qwT [K][E N].
+ *
+ * A forward and backward of y = sum_j weight_j expert_j(x) reads:
+ *   fp8rl_route_topk -> fp8rl_expert_rows -> fp8rl_expert_gather_quant(x) -> fp8rl_gemm_experts_fwd
+ *   -> fp8rl_silu_mul_quant -> fp8rl_gemm_experts_fwd -> fp8rl_expert_combine(weight);
+ *   fp8rl_expert_gather_quant(dout, weight) and fp8rl_expert_combine_dweight -> _dgrad, _wgrad ->
+ *   fp8rl_silu_mul_bwd_quant -> _dgrad, _wgrad -> fp8rl_expert_combine(no weight) is dx;
+ *   fp8rl_route_topk_bwd.
+ * -------------------------------------------------------------------------------------- */
+
+typedef enum { FP8RL_SCORE_SOFTMAX = 0, FP8RL_SCORE_SIGMOID = 1 } fp8rl_score;
+
+typedef struct {
+    const void* logits;   /* [T][ld], ld >= E: float, or BF16 with bf16 set */
+    int64_t ld;
+    int bf16;
+    int score;            /* fp8rl_score */
+    const float* bias;    /* [E], added to the scores for the selection only; NULL: none */
+    int k;                /* experts of a token, 1 .. min(E, 32) */
+    int n_groups;         /* equal groups of neighbouring experts (1 .. 32, divides E); 1: none */
+    int top_groups;       /* groups that a token may choose from */
+    int group_rank;       /* a group's rank is the sum of its 1 or 2 best */
+    int renormalize;      /* weights divided by (their sum + 1e-20) */
+    float scale;          /* multiplied into the weights */
+    float* weight;        /* out [T][k] */
+    int32_t* index;       /* out [T][k] */
+} fp8rl_route_args;
+
+/* The k experts of each token and their weights.  s = softmax or sigmoid of the logits,
+ * v = s + bias (the logits themselves where there is neither a bias nor a group_rank of 2, which
+ * gives the same order); among the experts of the top_groups best groups the k largest v, largest
+ * first, the lowest index first among equals.  The order is that of the exact values: scores too
+ * close for FP32 are compared in FP64.  weight = scale s / (sum of the k s + 1e-20), or scale s.
+ *   An expert whose logit or bias is -inf is never chosen; where fewer than k can be, the rest of
+ *   the row has index -1 and weight 0 (a padding token is a row of -inf).  NaN ranks above every
+ *   number, so that it shows in the weights.
+ * E <= 1024.  Pointers need the alignment of their elements only. */
+FP8RL_API fp8rl_status fp8rl_route_topk(const fp8rl_route_args* args, int64_t T, int64_t E, fp8rl_stream_t stream);
+
+typedef struct {
+    const float* dweight;   /* [T][k] */
+    const void* logits;     /* as in the forward */
+    int64_t ld;
+    int bf16;
+    int score;
+    const int32_t* index;   /* [T][k] the forward's; a value outside [0, E) is no expert */
+    int k;
+    int renormalize;
+    float scale;
+    void* dlogits;          /* out [T][ldd], ldd >= E, of the logits' type */
+    int64_t ldd;
+} fp8rl_route_bwd_args;
+
+/* The gradient of the logits from that of the weights (the selection and the bias have none).
+ * Experts given more than once in a row add up; masked logits get 0. */
+FP8RL_API fp8rl_status fp8rl_route_topk_bwd(const fp8rl_route_bwd_args* args, int64_t T, int64_t E,
+                                            fp8rl_stream_t stream);
+
+/* Expert order of the T k pairs p = t k + j.  Expert e has the rows start[e] .. start[e] +
+ * count[e], in the order of p; start[0] = 0 and start[e + 1] is the next multiple of `align` after
+ * them.  Every buffer of rows has R = fp8rl_expert_rows_capacity(T, k, E, align) rows, the most
+ * that the layout can need; rows that hold no pair are padding behind an expert or unused at the
+ * end.
+ *   align = 128: training and prefill (the 128x1 groups and the GEMM tiles of an expert are its own);
+ *   align = 1:   rollout, a few rows an expert (forward only; R = T k). */
+typedef struct {
+    const int32_t* pos;     /* [T][k] row of each pair, -1 for a pair of no expert */
+    const int32_t* src;     /* [R] pair of each row, or -1 */
+    const int32_t* start;   /* [E + 1] */
+    const int32_t* count;   /* [E] */
+    int64_t T, k, E, R, align;
+} fp8rl_expert_layout;
+
+/* R of a layout: the multiple of align at or below T k + min(E, T k) (align - 1); 0 where an
+ * argument is out of its range. */
+FP8RL_API int64_t fp8rl_expert_rows_capacity(int64_t T, int64_t k, int64_t E, int64_t align);
+
+/* Sorts the pairs by expert: index [T][k] -> pos, src, start, count (all written; start and src
+ * 16-byte aligned).  An index outside [0, E) is a pair of no expert; the same expert twice in a row
+ * is two pairs.  1 <= k <= 32, E <= 1024, T k <= 2^30, align 1 or 128.  The workspace, of
+ * fp8rl_expert_rows_workspace_bytes (0 for small calls), is written before it is read. */
+FP8RL_API fp8rl_status fp8rl_expert_rows(const int32_t* index, int64_t T, int64_t k, int64_t E, int64_t align,
+                                         int32_t* pos, int32_t* src, int32_t* start, int32_t* count, void* ws,
+                                         size_t ws_bytes, fp8rl_stream_t stream);
+FP8RL_API size_t fp8rl_expert_rows_workspace_bytes(int64_t T, int64_t k, int64_t E);
+
+/* Row src[r] / k of x for every row r, quantized as fp8rl_quantize_1x128 does.
+ *   x      : BF16 [T][ldx];  weight: float [T][k] or NULL: row r is bf16(weight[src[r]] x) then;
+ *   q, s   : E4M3 [R][K], float [K/128][R];
+ *   qT, sT : both NULL, or (align 128) the 128x1 quantization [K][R], [R/128][K].
+ * Every row is written: those of no pair have codes and scales 0. */
+FP8RL_API fp8rl_status fp8rl_expert_gather_quant(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
+                                                 const fp8rl_expert_layout* rows, uint8_t* q, float* s, uint8_t* qT,
+                                                 float* sT, fp8rl_stream_t stream);
+
+/* out[t] = residual[t] + sum_j weight[t][j] y[pos[t][j]], summed in FP32 in the order of j; weight
+ * NULL: 1; residual NULL: 0; pairs without a row add nothing.  With weight NULL it is the backward
+ * of the gather.
+ *   y : BF16 [R][ldy], residual [T][ldr], out [T][ldo], N columns, N % 8 == 0.  out may be residual. */
+FP8RL_API fp8rl_status fp8rl_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight,
+                                            const uint16_t* residual, int64_t ldr, const fp8rl_expert_layout* rows,
+                                            uint16_t* out, int64_t ldo, fp8rl_stream_t stream);
+
+/* dweight[t][j] = <dout[t], y[pos[t][j]]> in FP32, 0 for a pair without a row.  (The gradient of y
+ * is fp8rl_expert_gather_quant of dout with the weights.) */
+FP8RL_API fp8rl_status fp8rl_expert_combine_dweight(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t ldy,
+                                                    int64_t N, const fp8rl_expert_layout* rows, float* dweight,
+                                                    fp8rl_stream_t stream);
+
+/* Y[r] = X[r] W_e^T for the rows r of each expert e.  qx, sx as fp8rl_expert_gather_quant gives them;
+ * qw [E N][K], sw [E N / 128][K / 128]; y BF16 [R][N].  Rows behind the last expert's are left as
+ * they were, padding rows get the product of their codes.
+ *   align 128: 256 x 256 tiles on pairs of SMs;  align 1: a tile of 128 weight rows and up to 32
+ *   or 64 token rows, for up to some tens of rows an expert (it is right for any number). */
+FP8RL_API fp8rl_status fp8rl_gemm_experts_fwd(const uint8_t* qx, const float* sx, const uint8_t* qw, const float* sw,
+                                              uint16_t* y, int64_t N, int64_t K, const fp8rl_expert_layout* rows,
+                                              fp8rl_stream_t stream);
+
+/* dX[r] = dY[r] W_e.  qdy [R][N], sdy [N/128][R]; qwT [K][E N]; sw as above; dx BF16 [R][K].
+ * align 128. */
+FP8RL_API fp8rl_status fp8rl_gemm_experts_dgrad(const uint8_t* qdy, const float* sdy, const uint8_t* qwT, const float* sw,
+                                                uint16_t* dx, int64_t N, int64_t K, const fp8rl_expert_layout* rows,
+                                                fp8rl_stream_t stream);
+
+/* dW_e = sum over the rows r of expert e of dY[r]^T X[r], zeros for an expert without rows.
+ * qdyT [N][R], sdyT [R/128][N], qxT [K][R], sxT [R/128][K]; dw BF16 [E N][K].  align 128. */
+FP8RL_API fp8rl_status fp8rl_gemm_experts_wgrad(const uint8_t* qdyT, const float* sdyT, const uint8_t* qxT,
+                                                const float* sxT, uint16_t* dw, int64_t N, int64_t K,
+                                                const fp8rl_expert_layout* rows, fp8rl_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
  * Diagnostics (used by the tests).
  * -------------------------------------------------------------------------------------- */
 
