@@ -13,9 +13,10 @@
 // (score_error), and a row in which two neighbours of the order, or the groups' border, are too
 // close for that is decided again from FP64 scores.
 //
-// One warp per row; lane l holds experts l, l + 32, ..., whose comparisons run on integers that
-// order as the values do (0: cannot be selected), so a step of the selection is two redux
-// instructions and a scan of the lane's own values.
+// One warp per row; lane l holds the NL neighbouring experts from l NL on, whose comparisons run on
+// integers that order as the values do (0: cannot be selected), so a step of the selection is a
+// scan of the lane's own values, a redux and a ballot.  The lowest lane, and in it the lowest place,
+// is the lowest index.
 #include "common.cuh"
 #include "experts.h"
 
@@ -60,86 +61,140 @@ __device__ __forceinline__ float sigmoid_f(float z) { return __frcp_rn(1.0f + ex
 // Group of expert e, from mul = ceil(2^22 / group size): exact for e < 1024.
 __device__ __forceinline__ uint32_t group_of(uint32_t e, uint32_t mul) { return (e * mul) >> 22; }
 
-// FP64 selection of one row (rows with a near tie).  order[j] of lane j: the j-th expert.
+// Keys of FP64 values: (hi, lo) order as the values do, 0 for -inf; NaN above all.
+__device__ __forceinline__ uint64_t order_key64(double v) {
+    if (v != v) return ~0ull;
+    if (v == -INFINITY) return 0ull;
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+    return (b >> 63) ? ~b : (b | (1ull << 63));
+}
+__device__ __forceinline__ double key_value64(uint64_t k) {
+    return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+}
+__device__ __forceinline__ uint32_t reduce_max(uint32_t k) { return __reduce_max_sync(kFull, k); }
+__device__ __forceinline__ uint64_t reduce_max(uint64_t k) {
+    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(k >> 32));
+    const uint32_t lo = __reduce_max_sync(kFull, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return ((uint64_t)hi << 32) | lo;
+}
+__device__ __forceinline__ uint32_t key_sum(uint32_t a, uint32_t b) { return order_key(key_value(a) + key_value(b)); }
+__device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key64(key_value64(a) + key_value64(b)); }
+
+// Zeroes the keys of the experts outside the top_groups best groups.  Returns the ranks of the
+// worst group kept and the best one left (0 if none is left).
+template <int NL, typename KEY>
+__device__ __forceinline__ void keep_groups(const fp8rl_route_args& a, int E, uint32_t gs_mul, int lane, KEY (&key)[NL], KEY* worst, KEY* left) {
+    const int G = a.n_groups, gs = E / G;
+    const int lpg = gs / NL;                            // lanes of a group
+    KEY score = 0;                                      // lane g: rank of group g
+    if (gs % NL == 0 && (lpg & (lpg - 1)) == 0) {
+        // every group is lpg neighbouring lanes: its two best in log2(lpg) exchanges
+        KEY b1 = 0, b2 = 0;
+        #pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            b2 = max(b2, min(b1, key[i]));
+            b1 = max(b1, key[i]);
+        }
+        for (int o = 1; o < lpg; o <<= 1) {
+            const KEY o1 = __shfl_xor_sync(kFull, b1, o), o2 = __shfl_xor_sync(kFull, b2, o);
+            b2 = max(max(b2, o2), min(b1, o1));
+            b1 = max(b1, o1);
+        }
+        if (a.group_rank == 2 && b2 != 0) b1 = key_sum(b1, b2);
+        score = __shfl_sync(kFull, b1, (lane * lpg) & 31);
+    } else {
+        for (int g = 0; g < G; ++g) {
+            KEY b1 = 0, b2 = 0;
+            #pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const KEY k = group_of((uint32_t)(lane * NL + i), gs_mul) == (uint32_t)g ? key[i] : 0;
+                b2 = max(b2, min(b1, k));
+                b1 = max(b1, k);
+            }
+            KEY t = reduce_max(b1);
+            if (a.group_rank == 2) {
+                const uint32_t holder = __ballot_sync(kFull, b1 == t);
+                const KEY second = reduce_max(lane == __ffs(holder) - 1 ? b2 : b1);
+                if (second != 0) t = key_sum(t, second);
+            }
+            if (lane == g) score = t;
+        }
+    }
+    int before = 0;
+    for (int g = 0; g < G; ++g) {
+        const KEY o = __shfl_sync(kFull, score, g);
+        before += (o > score || (o == score && g < lane)) ? 1 : 0;
+    }
+    const bool kept = lane < G && before < a.top_groups;
+    const uint32_t keep = __ballot_sync(kFull, kept);
+    if (worst) {
+        *worst = ~reduce_max(kept ? (KEY)~score : (KEY)0);
+        *left = reduce_max(!kept && lane < G ? score : (KEY)0);
+    }
+    #pragma unroll
+    for (int i = 0; i < NL; ++i)
+        if (!((keep >> (group_of((uint32_t)(lane * NL + i), gs_mul) & 31u)) & 1u)) key[i] = 0;
+}
+
+// The largest key left, and its expert if there is one (0: none): the expert's key is zeroed.
+template <int NL, typename KEY>
+__device__ __forceinline__ KEY take_best(KEY (&key)[NL], int lane, int* expert) {
+    KEY b = key[0];
+    #pragma unroll
+    for (int i = 1; i < NL; ++i) b = max(b, key[i]);
+    const KEY top = reduce_max(b);
+    if (top == 0) return 0;
+    const int owner = __ffs(__ballot_sync(kFull, b == top)) - 1;
+    int at = 0;
+    #pragma unroll
+    for (int i = NL - 1; i >= 0; --i)
+        if (key[i] == top) at = i;
+    #pragma unroll
+    for (int i = 0; i < NL; ++i)
+        if (lane == owner && i == at) key[i] = 0;
+    *expert = __shfl_sync(kFull, lane * NL + at, owner);
+    return top;
+}
+
+// The selection of one row from FP64 scores (rows with a near tie): lane j returns the j-th expert.
 template <int NL, bool BF16>
-__device__ __noinline__ int select_f64(const fp8rl_route_args& a, int64_t row, int E, int lane) {
-    double v[NL];
+__device__ __noinline__ int select_f64(const fp8rl_route_args& a, int64_t row, int E, uint32_t gs_mul, int lane) {
     const bool sm = a.score == FP8RL_SCORE_SOFTMAX;
     const int64_t base = row * a.ld;
+    double v[NL];
+    uint64_t key[NL];
     float m = -INFINITY;
+    #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < E) m = fmaxf(m, load_logit<BF16>(a.logits, base + e));
+        const int e = lane * NL + i;
+        const float z = e < E ? load_logit<BF16>(a.logits, base + e) : -INFINITY;
+        m = fmaxf(m, z);
+        v[i] = (double)z;
+        key[i] = z == -INFINITY ? 0ull : 1ull;      // 1: may be selected
     }
     m = warp_max(m);
     double sum = 0.0;
+    #pragma unroll 1
     for (int i = 0; i < NL; ++i) {
-        const int e = i * 32 + lane;
-        const double z = e < E ? (double)load_logit<BF16>(a.logits, base + e) : -INFINITY;
-        v[i] = sm ? exp(z - (double)m) : 1.0 / (1.0 + exp(-z));
-        if (e < E) sum += v[i];
+        if (key[i]) v[i] = sm ? exp(v[i] - (double)m) : 1.0 / (1.0 + exp(-v[i]));
+        if (key[i]) sum += v[i];
     }
-    sum = warp_sum(sum);
+    if (sm) sum = warp_sum(sum);
+    #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        const int e = i * 32 + lane;
-        if (sm) v[i] /= sum;
-        if (e < E && a.bias) v[i] += (double)__ldg(a.bias + e);
-        if (e >= E || load_logit<BF16>(a.logits, base + e) == -INFINITY) v[i] = -INFINITY;
-        if (v[i] != v[i]) v[i] = INFINITY;      // NaN first
+        const int e = lane * NL + i;
+        double x = sm ? v[i] / sum : v[i];
+        if (a.bias && e < E) x += (double)__ldg(a.bias + e);
+        if (key[i]) key[i] = order_key64(x);
     }
-    // the largest of the warp below or at (value, index) limits: lowest index among equals
-    auto best = [&](double mine, int idx) {
-        for (int o = 16; o >= 1; o >>= 1) {
-            const double ov = __shfl_xor_sync(kFull, mine, o);
-            const int oi = __shfl_xor_sync(kFull, idx, o);
-            if (ov > mine || (ov == mine && oi < idx)) { mine = ov; idx = oi; }
-        }
-        return make_double2(mine, (double)idx);
-    };
-    if (a.n_groups > 1) {
-        const int gs = E / a.n_groups;
-        double score = -INFINITY;
-        for (int g = 0; g < a.n_groups; ++g) {
-            double tot = -INFINITY;
-            int taken = -1;
-            for (int r = 0; r < a.group_rank; ++r) {
-                double mine = -INFINITY;
-                int idx = 1 << 20;
-                for (int i = 0; i < NL; ++i) {
-                    const int e = i * 32 + lane;
-                    if (e / gs == g && e != taken && v[i] > mine) { mine = v[i]; idx = e; }
-                }
-                const double2 b = best(mine, idx);
-                if (b.x != -INFINITY) tot = tot == -INFINITY ? b.x : tot + b.x;
-                taken = (int)b.y;
-            }
-            if (lane == g) score = tot;
-        }
-        int before = 0;
-        for (int g = 0; g < a.n_groups; ++g) {
-            const double o = __shfl_sync(kFull, score, g);
-            before += (o > score || (o == score && g < lane)) ? 1 : 0;
-        }
-        const uint32_t keep = __ballot_sync(kFull, lane < a.n_groups && before < a.top_groups);
-        for (int i = 0; i < NL; ++i) {
-            const int e = i * 32 + lane;
-            if (e < E && !((keep >> (e / gs)) & 1u)) v[i] = -INFINITY;
-        }
-    }
-    int got = -1;
+    if (a.n_groups > 1) keep_groups<NL, uint64_t>(a, E, gs_mul, lane, key, nullptr, nullptr);
+    int mine = -1;
     for (int j = 0; j < a.k; ++j) {
-        double mine = -INFINITY;
-        int idx = 1 << 20;
-        for (int i = 0; i < NL; ++i)
-            if (v[i] > mine) { mine = v[i]; idx = i * 32 + lane; }
-        const double2 b = best(mine, idx);
-        const int e = (int)b.y;
-        if (b.x == -INFINITY) break;
-        if (lane == j) got = e;
-        for (int i = 0; i < NL; ++i)
-            if (i * 32 + lane == e) v[i] = -INFINITY;
+        int e = 0;
+        if (take_best<NL, uint64_t>(key, lane, &e) == 0) break;
+        if (lane == j) mine = e;
     }
-    return got;
+    return mine;
 }
 
 // How far an FP32 v may be from its value, the largest score of the row being smax.  A sigmoid is
@@ -161,7 +216,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const fp8rl_route_ar
     float z[NL];
     #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        const int e = i * 32 + lane;
+        const int e = lane * NL + i;
         z[i] = e < E ? load_logit<BF16>(a.logits, base + e) : -INFINITY;
     }
     // softmax: the row's maximum and sum, where something needs the scores of all experts
@@ -175,14 +230,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const fp8rl_route_ar
             float t = 0.0f;
             #pragma unroll
             for (int i = 0; i < NL; ++i)
-                if (i * 32 + lane < E) t += expf(z[i] - m);
+                if (lane * NL + i < E) t += expf(z[i] - m);
             inv = 1.0f / warp_sum(t);
         }
     }
     uint32_t key[NL];
     #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        const int e = i * 32 + lane;
+        const int e = lane * NL + i;
         float v = z[i];
         if (!by_logit && e < E && z[i] != -INFINITY) {
             v = sm ? expf(z[i] - m) * inv : sigmoid_f(z[i]);
@@ -193,71 +248,37 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const fp8rl_route_ar
     const float smax = sm ? inv : 1.0f;      // no score is larger
     bool close = false;
     if (a.n_groups > 1) {
-        // lane g keeps the score of group g; its experts' groups are e / (E / n_groups)
-        uint32_t score = 0;
-        for (int g = 0; g < a.n_groups; ++g) {
-            uint32_t b1 = 0, b2 = 0;
-            #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const uint32_t k = group_of((uint32_t)(i * 32 + lane), gs_mul) == (uint32_t)g ? key[i] : 0u;
-                b2 = max(b2, min(b1, k));
-                b1 = max(b1, k);
-            }
-            uint32_t s = __reduce_max_sync(kFull, b1);
-            if (a.group_rank == 2) {
-                const uint32_t holder = __ballot_sync(kFull, b1 == s);
-                const uint32_t second = __reduce_max_sync(kFull, lane == __ffs(holder) - 1 ? b2 : b1);
-                if (second != 0 && s != 0) s = order_key(key_value(s) + key_value(second));
-            }
-            if (lane == g) score = s;
-        }
-        int before = 0;
-        for (int g = 0; g < a.n_groups; ++g) {
-            const uint32_t o = __shfl_sync(kFull, score, g);
-            before += (o > score || (o == score && g < lane)) ? 1 : 0;
-        }
-        const bool kept = lane < a.n_groups && before < a.top_groups;
-        const uint32_t keep = __ballot_sync(kFull, kept);
-        if (!by_logit) {
-            const uint32_t lo = __reduce_min_sync(kFull, kept ? score : 0xffffffffu);
-            const uint32_t hi = __reduce_max_sync(kFull, !kept && lane < a.n_groups ? score : 0u);
-            if (hi != 0) {
-                // sums of two: twice the error on each side, and their own rounding
-                const float v = key_value(lo);
-                close = !(v - key_value(hi) > 6.0f * score_error(v, smax, sm));
-            }
-        }
-        #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const uint32_t g = group_of((uint32_t)(i * 32 + lane), gs_mul);
-            if (!((keep >> (g & 31)) & 1u)) key[i] = 0;
+        uint32_t worst, left;
+        keep_groups<NL, uint32_t>(a, E, gs_mul, lane, key, &worst, &left);
+        if (!by_logit && left != 0) {
+            // sums of two: twice the error on each side, and their own rounding
+            const float v = key_value(worst);
+            close = !(v - key_value(left) > 6.0f * score_error(v, smax, sm));
         }
     }
     int mine = -1;              // lane j: the j-th expert
     uint32_t last = 0;
-    for (int j = 0; j <= a.k; ++j) {
-        uint32_t b = 0;
-        #pragma unroll
-        for (int i = 0; i < NL; ++i) b = max(b, key[i]);
-        const uint32_t top = __reduce_max_sync(kFull, b);
+    for (int j = 0; j < a.k; ++j) {
+        int e = 0;
+        const uint32_t top = take_best<NL, uint32_t>(key, lane, &e);
         if (top == 0) break;
+        if (lane == j) mine = e;
         if (j > 0 && !by_logit) {
             const float v = key_value(last);
             close = close || !(v - key_value(top) > 3.0f * score_error(v, smax, sm));
         }
         last = top;
-        if (j == a.k) break;
-        uint32_t idx = 0x7fffffffu;
-        #pragma unroll
-        for (int i = NL - 1; i >= 0; --i)
-            if (key[i] == top) idx = i * 32 + lane;
-        idx = __reduce_min_sync(kFull, idx);
-        #pragma unroll
-        for (int i = 0; i < NL; ++i)
-            if ((uint32_t)(i * 32 + lane) == idx) key[i] = 0;
-        if (lane == j) mine = (int)idx;
     }
-    if (close) mine = select_f64<NL, BF16>(a, row, E, lane);
+    if (!by_logit && last != 0) {
+        // the best of those not taken (if any) against the last one taken
+        uint32_t b = key[0];
+        #pragma unroll
+        for (int i = 1; i < NL; ++i) b = max(b, key[i]);
+        b = __reduce_max_sync(kFull, b);
+        const float v = key_value(last);
+        close = close || (b != 0 && !(v - key_value(b) > 3.0f * score_error(v, smax, sm)));
+    }
+    if (close) mine = select_f64<NL, BF16>(a, row, E, gs_mul, lane);
     float s = 0.0f;
     if (mine >= 0) {
         const float zz = load_logit<BF16>(a.logits, base + mine);
