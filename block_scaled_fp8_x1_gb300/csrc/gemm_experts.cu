@@ -16,10 +16,10 @@
 // memory.  A segment with an odd number of 128-row blocks leaves half of its last pair tile unused
 // (computed on the next expert's rows, not stored).
 //
-// Roles and pipeline as in gemm_pair.cu: warp 0 copies, warp 1 issues the MMAs, 8 (forward, DGrad)
-// or 16 (WGrad) epilogue warps promote each K-block's partial sums from one of two 256-column TMEM
-// buffers.  B's block scales are one number per K-block and 128 columns: a warp loads those of 32
-// K-blocks at once, one a lane, 32 K-blocks ahead, so any number of K-blocks will do.
+// Roles and pipeline as in gemm_pair.cu: warp 0 copies the operands, warp 3 the scales, warp 1
+// issues the MMAs, 8 (forward, DGrad) or 16 (WGrad) epilogue warps promote each K-block's partial
+// sums from one of two 256-column TMEM buffers.  B's block scales come by 4-byte copies, so that any
+// number of K-blocks and columns will do.
 // Every mbarrier wait is bounded (FP8RL_ERR_DEVICE_TIMEOUT).
 #include "common.cuh"
 #include "experts.h"
@@ -30,7 +30,6 @@ namespace {
 
 constexpr int kPN = 256;         // columns of a pair tile
 constexpr int kBufs = 2;         // TMEM buffers of kPN columns
-constexpr int kStages = 5;
 
 // Register split as in gemm_pair.cu.
 __host__ __device__ constexpr int x_threads(int epi) { return 128 + 32 * epi; }
@@ -39,11 +38,11 @@ __host__ __device__ constexpr uint32_t x_reg_lo(int epi) { return epi == 16 ? 32
 __host__ __device__ constexpr uint32_t x_reg_hi(int epi) { return epi == 16 ? 112 : 224; }
 static_assert(128 * x_reg_lo(8) + 256 * x_reg_hi(8) <= x_threads(8) * x_launch_regs(8), "split");
 static_assert(128 * x_reg_lo(16) + 512 * x_reg_hi(16) <= x_threads(16) * x_launch_regs(16), "split");
-__host__ __device__ constexpr int x_boxes(int epi) { return epi == 16 ? 1 : 2; }
 
 template <bool WGRAD>
 struct XSmem {
     static constexpr int EPI = WGRAD ? 16 : 8;
+    static constexpr int STAGES = 4;
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = (kPN / 2) * 128;
     static constexpr int SG = WGRAD ? 1 : 4;              // K-blocks of a scale slot
@@ -51,10 +50,10 @@ struct XSmem {
     static constexpr int SLOT_A = 128 * SG;               // floats
     static constexpr int SLOT = SLOT_A + (WGRAD ? kPN : 0);
     static constexpr int RING_BYTES = NS * SLOT * 4;
-    static constexpr int STAGE_C_BYTES = EPI * x_boxes(EPI) * 2048;
-    static constexpr int NBARS = 2 * kStages + 2 * kBufs + 2 * NS + 1;
+    static constexpr int STAGE_C_BYTES = 128 * kPN * 2;      // the whole result tile, 2 KB boxes
+    static constexpr int NBARS = 2 * STAGES + 2 * kBufs + 2 * NS + 1;
     static size_t bytes(int E) {
-        return 1024 + (size_t)kStages * (A_BYTES + B_BYTES) + STAGE_C_BYTES + RING_BYTES + NBARS * 8 + 16 +
+        return 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + STAGE_C_BYTES + RING_BYTES + NBARS * 8 + 16 +
                2 * (size_t)(E + 1) * 4;
     }
 };
@@ -74,38 +73,54 @@ template <bool WGRAD>
 struct XWalk {
     const int32_t* start;     // [E + 1]
     const int32_t* tiles;     // forward, DGrad: [E + 1] tiles of the experts before
-    int E, n_tiles, rows, nkb, e;
+    int E, n_tiles, rows, nkb;
+    int e, before;            // current expert, WGrad: tiles of the experts before it
     __device__ __forceinline__ int total() const {
         return WGRAD ? E * ((rows + 255) / 256) * n_tiles : tiles[E];
+    }
+    // WGrad: advances to the expert of `item` and returns its K-blocks (else the constant)
+    __device__ __forceinline__ int blocks(int item) {
+        if (!WGRAD) return nkb;
+        const int per = ((rows + 255) / 256) * n_tiles;
+        while (item - before >= per) {
+            before += per;
+            ++e;
+        }
+        return max(0, start[e + 1] - start[e]) >> 7;
     }
     __device__ __forceinline__ XTile at(int item, int rank) {
         XTile t;
         int m, n, units;
         if (WGRAD) {
+            t.nkb = blocks(item);
+            item -= before;
             units = (rows + 255) / 256;
-            const int per = units * n_tiles;
-            e = item / per;
-            item -= e * per;
         } else {
+            t.nkb = nkb;
             while (tiles[e + 1] <= item) ++e;
             item -= tiles[e];
             units = (start[e + 1] - start[e] + 255) / 256;
         }
-        // within an expert: 16 row units at a time sweep the columns, which keeps their rows (16 MB
-        // at 4096 columns) and the expert's weights in L2
-        raster_tile(item, units, n_tiles, 16, 0, &m, &n);
+        // within an expert 16 row units at a time sweep the columns, which keeps their rows (16 MB
+        // at 4096 columns) and the expert's weights in L2.  Up to 16 units that is one division,
+        // which a reciprocal gives exactly (item * units < 2^22): the warps compute it between two
+        // tiles, where an integer division's latency showed.
+        if (units <= 16) {
+            n = (int)(((float)item + 0.5f) * __frcp_rn((float)units));
+            m = item - n * units;
+        } else {
+            raster_tile(item, units, n_tiles, 16, 0, &m, &n);
+        }
         t.e = e;
         t.col = n * kPN;
         if (WGRAD) {
             t.row = m * 256 + rank * 128;
             t.row_end = rows;
             t.kb0 = start[e] >> 7;
-            t.nkb = max(0, start[e + 1] - start[e]) >> 7;
         } else {
             t.row = start[e] + m * 256 + rank * 128;
             t.row_end = start[e + 1];
             t.kb0 = 0;
-            t.nkb = nkb;
         }
         return t;
     }
@@ -117,7 +132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                    const __grid_constant__ CUtensorMap tmC, const ExpertGemmParams p) {
     using S = XSmem<WGRAD>;
-    constexpr int EPI = S::EPI, NS = S::NS;
+    constexpr int EPI = S::EPI, NS = S::NS, kStages = S::STAGES;
     constexpr int COLS = kPN / (EPI / 4);           // columns per epilogue thread
     constexpr uint32_t TMEM_COLS = 512;
     constexpr uint32_t IDESC = idesc_e4m3_f32(256, kPN);
@@ -202,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
     cluster_sync_all();   // both CTAs' barriers initialised, TMEM allocated, starts in place
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    XWalk<WGRAD> walk{s_start, s_tiles, p.E, n_tiles, p.rows, p.nkb, 0};
+    XWalk<WGRAD> walk{s_start, s_tiles, p.E, n_tiles, p.rows, p.nkb, 0, 0};
     const int num_items = walk.total();
 
     if (warp < 4) {
@@ -211,8 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             // ------------------------------------------------------------ copies
             const uint64_t pol = l2_policy_evict_last();
             const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);   // the leader's
-            const int sgrp = WGRAD ? 1 : (p.nkb < S::SG ? p.nkb : S::SG);
-            uint32_t it = 0, s_issued = 0;
+            uint32_t it = 0;
             bool ok = true;
             for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
                 const XTile t = walk.at(item, (int)rank);
@@ -225,26 +239,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                         ok = false;
                         break;
                     }
-                    const bool g_first = kb % S::SG == 0;
-                    const uint32_t ss = s_issued % NS;
-                    if (g_first && !mbar_wait(smem_u32(&sempty_bar[ss]), ((s_issued / NS) & 1) ^ 1, p.timeout_ns, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
                     if (elect_one_sync()) {
                         if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * (S::A_BYTES + S::B_BYTES));
                         tma_load_2d_pair(smem_u32(sA + s * S::A_BYTES), &tmA, full0 + 8 * s, ax + kb * 128, t.row, pol);
                         tma_load_2d_pair(smem_u32(sB + s * S::B_BYTES), &tmB, full0 + 8 * s, bx + kb * 128, by, pol);
-                        if (g_first) {
-                            const uint32_t sb = smem_u32(&sfull_bar[ss]);
-                            float* slot = ring + ss * S::SLOT;
-                            mbar_arrive_expect_tx(sb, 128u * 4u * (uint32_t)sgrp + (WGRAD ? (uint32_t)kPN * 4u : 0u));
-                            tma_load_2d(smem_u32(slot), &tmSA, sb, t.row, t.kb0 + kb, pol);
-                            if (WGRAD) tma_load_2d(smem_u32(slot + S::SLOT_A), &tmSB, sb, t.col, t.kb0 + kb, pol);
-                        }
                     }
                     __syncwarp();
-                    if (g_first) ++s_issued;
                 }
             }
             // Drain: the copies issued here land before the CTA can exit.
@@ -254,8 +254,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                 for (uint32_t j = it - n_out; j < it; ++j)
                     mbar_wait(smem_u32(&full_bar[j % kStages]), (j / kStages) & 1, p.timeout_ns, &no_abort);
             }
-            const uint32_t s_out = s_issued < (uint32_t)NS ? s_issued : (uint32_t)NS;
-            for (uint32_t j = s_issued - s_out; j < s_issued; ++j)
+        } else if (warp == 3) {
+            // ------------------------------------------------------------ scales
+            // a warp of their own, so that they run ahead of the operands by the whole scale ring
+            // (16 K-blocks): B's come one by one from rows far apart, and with the operands' lead
+            // of 5 K-blocks the epilogue waited for them
+            const uint64_t pol = l2_policy_evict_last();
+            const int sgrp = WGRAD ? 1 : (p.nkb < S::SG ? p.nkb : S::SG);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
+                const XTile t = walk.at(item, (int)rank);
+                for (int kb = 0; kb < t.nkb; kb += S::SG, ++it) {
+                    const uint32_t ss = it % NS;
+                    if (!mbar_wait(smem_u32(&sempty_bar[ss]), ((it / NS) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sb = smem_u32(&sfull_bar[ss]);
+                    float* slot = ring + ss * S::SLOT;
+                    if (elect_one_sync()) {
+                        mbar_arrive_expect_tx(sb, 128u * 4u * (uint32_t)sgrp + (WGRAD ? (uint32_t)kPN * 4u : 0u));
+                        tma_load_2d(smem_u32(slot), &tmSA, sb, t.row, t.kb0 + kb, pol);
+                        if (WGRAD) tma_load_2d(smem_u32(slot + S::SLOT_A), &tmSB, sb, t.col, t.kb0 + kb, pol);
+                    }
+                    __syncwarp();
+                }
+            }
+            volatile int no_abort = 0;
+            const uint32_t n_out = it < (uint32_t)NS ? it : (uint32_t)NS;
+            for (uint32_t j = it - n_out; j < it; ++j)
                 mbar_wait(smem_u32(&sfull_bar[j % NS]), (j / NS) & 1, p.timeout_ns, &no_abort);
         } else if (warp == 1 && leader) {
             // ------------------------------------------------------------ MMA issuer
@@ -263,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             bool ok = true;
             const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
             for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
-                const int nkb = walk.at(item, 0).nkb;
+                const int nkb = walk.blocks(item);
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const uint32_t ts = it % kBufs;
                     const uint32_t s = it % kStages;
@@ -300,13 +328,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
         const int col_base = (ew >> 2) * COLS;   // first column of this thread
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty_bar), 0);   // the leader's
-        constexpr int NBX = x_boxes(EPI);
         // block scale of K-block kb of B for this warp's 128 columns of tile t (0 outside)
         auto b_scale = [&](const XTile& t, int kb) {
             const int cb = (t.col + col_base) >> 7;
             return kb < t.nkb && cb * 128 < p.cols ? __ldg(p.sb + t.e * p.sb_e + cb * p.sb_c + kb * p.sb_kb) : 0.0f;
         };
-        uint32_t acc_it = 0, g_done = 0, box_it = 0;
+        uint32_t acc_it = 0, g_done = 0;
         bool ok = true;
         XTile t = {};
         float sb_cur = 0.0f, sb_nxt = 0.0f;      // lane l: the scale of K-block l of 32
@@ -316,8 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
         }
         for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
             const bool more = item + (int)ncl < num_items;
-            XTile next = t;
-            if (!WGRAD && more) next = walk.at(item + (int)ncl, (int)rank);
+            const XTile next = more ? walk.at(item + (int)ncl, (int)rank) : t;
             float2 acc[COLS / 2];
             #pragma unroll
             for (int c = 0; c < COLS / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
@@ -431,11 +457,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             // are not stored.
             const int y0 = t.row + quad * 32;
             const int yc = (WGRAD ? t.e * p.rows : 0) + y0;
+            if (lane == 0) bulk_wait_read<0>();      // the previous tile's stores have read the boxes
+            __syncwarp();
             #pragma unroll
-            for (int b = 0; b < COLS / 32; ++b, ++box_it) {
-                const uint32_t buf = smem_u32(stage_c + (ew * NBX + (int)(box_it % NBX)) * 2048);
-                if (lane == 0) bulk_wait_read<NBX - 1>();
-                __syncwarp();
+            for (int b = 0; b < COLS / 32; ++b) {
+                const uint32_t buf = smem_u32(stage_c + (ew * (COLS / 32) + b) * 2048);
                 if constexpr (WGRAD) {
                     // rows g + 8h, columns 8j + 2tq + {0,1}: one BF16 pair per (row, chunk)
                     const int g8 = lane >> 2, tq = lane & 3;
@@ -460,16 +486,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                         st_shared_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v);
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    const int x = t.col + col_base + b * 32;
-                    if (y0 < t.row_end && x < p.cols) tma_store_2d(&tmC, buf, x, yc);
-                    bulk_commit();
-                }
             }
-            if (!WGRAD) t = next;
-            else if (more) t = walk.at(item + (int)ncl, (int)rank);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                #pragma unroll
+                for (int b = 0; b < COLS / 32; ++b) {
+                    const int x = t.col + col_base + b * 32;
+                    if (y0 < t.row_end && x < p.cols)
+                        tma_store_2d(&tmC, smem_u32(stage_c + (ew * (COLS / 32) + b) * 2048), x, yc);
+                }
+                bulk_commit();
+            }
+            t = next;
         }
         if (lane == 0) bulk_wait_all();   // tile stores complete before exit
     }
