@@ -1350,7 +1350,7 @@ fp8rl_status fp8rl_expert_rows(const int32_t* index, int64_t T, int64_t k, int64
 fp8rl_status fp8rl_expert_gather_quant(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
                                        const fp8rl_expert_layout* rows, uint8_t* q, float* s, uint8_t* qT, float* sT,
                                        fp8rl_stream_t stream) {
-    fp8rl_status e = check_layout(rows, "s");
+    fp8rl_status e = check_layout(rows, "ps");
     if (e != FP8RL_OK) return e;
     if (K <= 0 || ldx < K || (qT == nullptr) != (sT == nullptr)) return FP8RL_ERR_INVALID_ARG;
     if (K % 128 != 0 || (qT && rows->align != kExpertAlign)) return FP8RL_ERR_SHAPE;
@@ -1361,8 +1361,7 @@ fp8rl_status fp8rl_expert_gather_quant(const uint16_t* x, int64_t ldx, int64_t K
         return FP8RL_ERR_ALIGN;
     int sms = 0;
     if ((e = current_device(&sms)) != FP8RL_OK) return e;
-    if (qT) return cuda_status(launch_expert_gather_dual(x, ldx, K, weight, *rows, q, s, qT, sT, g_timeout_ns.load(), stream));
-    return cuda_status(launch_expert_gather_rows(x, ldx, K, weight, *rows, q, s, sms, stream));
+    return cuda_status(launch_expert_gather(x, ldx, K, weight, *rows, q, s, qT, sT, sms, g_timeout_ns.load(), stream));
 }
 
 fp8rl_status fp8rl_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,

@@ -1,5 +1,5 @@
-// expert_rows.cu -- between token order and expert order: the stable sort of (token, expert) pairs,
-// the gather of token rows into it with their 1x128 quantization, and the weighted sum back.
+// expert_rows.cu -- between token order and expert order: the stable sort of (token, expert) pairs and
+// the weighted sum back (the gather is in quantize.cu).
 //
 // Row layout (fp8rl_expert_layout): expert e's pairs, in the order of p = t k + j, take rows
 // start[e] .. start[e] + count[e]; start[e + 1] is the next multiple of `align` after them.
@@ -139,52 +139,6 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_place(const int32_t*
     for (int64_t r = (int64_t)s_start[E] + (int64_t)b * blockDim.x + tid; r < R; r += (int64_t)nb * blockDim.x) src[r] = -1;
 }
 
-// ---------------------------------------------------------------- gather + quantize
-
-// Rows in expert order, 1x128: 16 threads a group of 128 as in k_quant_1x128, the groups numbered
-// block-major so that neighbouring groups' scales are stored together.  A weighted row is rounded to
-// BF16 before it is quantized, as the gradient between operators is.  Rows without a pair give zeros.
-__global__ void __launch_bounds__(256) k_expert_gather_rows(const uint16_t* __restrict__ x, int64_t ldx, int64_t K,
-                                                            const float* __restrict__ weight, const int32_t* __restrict__ src,
-                                                            int64_t T, int k, int64_t R, uint8_t* __restrict__ q,
-                                                            float* __restrict__ s) {
-    const int sub = threadIdx.x & 15;
-    const int half = (threadIdx.x >> 4) & 1;
-    const int warp = threadIdx.x >> 5;
-    const int64_t ngroups = R * (K / 128);
-    const int64_t step = (int64_t)gridDim.x * 16;
-    for (int64_t base = (int64_t)blockIdx.x * 16 + warp * 2; base < ngroups; base += step) {
-        const int64_t g = base + half;
-        const bool valid = g < ngroups;
-        const int64_t kb = valid ? g / R : 0;
-        const int64_t r = valid ? g - kb * R : 0;
-        const int p = __ldg(src + r);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (valid && p >= 0 && p < T * k) {
-            v = ldg_v4(x + (int64_t)(p / k) * ldx + kb * 128 + sub * 8);
-            if (weight) {
-                const float w = __ldg(weight + p);
-                uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-                #pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] = pack_bf16x2(bf16_lo(u[j]) * w, bf16_hi(u[j]) * w);
-            }
-        }
-        uint32_t mx = absmax2(absmax2(absmax2(absmax2(0u, v.x), v.y), v.z), v.w);
-        mx = max(mx & 0xFFFFu, mx >> 16);
-        #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) mx = max(mx, __shfl_xor_sync(kFull, mx, off));
-        const GroupScale gs = make_scale(bf16_bits_amax_to_f32(mx));
-        const uint32_t c0 = encode_pair(bf16_lo(v.x), bf16_hi(v.x), gs);
-        const uint32_t c1 = encode_pair(bf16_lo(v.y), bf16_hi(v.y), gs);
-        const uint32_t c2 = encode_pair(bf16_lo(v.z), bf16_hi(v.z), gs);
-        const uint32_t c3 = encode_pair(bf16_lo(v.w), bf16_hi(v.w), gs);
-        if (valid) {
-            *reinterpret_cast<uint2*>(q + r * K + kb * 128 + sub * 8) = make_uint2(c0 | (c1 << 16), c2 | (c3 << 16));
-            if (sub == 0) s[kb * R + r] = gs.s;
-        }
-    }
-}
-
 // ---------------------------------------------------------------- combine
 
 // out[t] = residual[t] + sum_j weight[t, j] y[pos[t, j]] in FP32 in the order of j: a thread has 8
@@ -280,14 +234,6 @@ cudaError_t launch_expert_rows(const int32_t* index, int64_t P, int E, int align
                                          (int)(((size_t)kSortWarps + 2) * kMaxExperts * 4 + 4));
     if (e != cudaSuccess) return e;
     k_expert_place<<<nb, 32 * kSortWarps, smem, st>>>(index, P, E, chunk, align, R, hist, pos, src, start, count);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_expert_gather_rows(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
-                                      const fp8rl_expert_layout& l, uint8_t* q, float* s, int num_sms, cudaStream_t st) {
-    const int64_t ngroups = l.R * (K / 128);
-    const int64_t blocks = std::min<int64_t>((ngroups + 15) / 16, (int64_t)num_sms * 16);
-    k_expert_gather_rows<<<(unsigned)blocks, 256, 0, st>>>(x, ldx, K, weight, l.src, l.T, (int)l.k, l.R, q, s);
     return cudaGetLastError();
 }
 

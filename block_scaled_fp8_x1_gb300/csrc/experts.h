@@ -22,17 +22,15 @@ cudaError_t launch_route_topk_bwd(const fp8rl_route_bwd_args& a, int64_t T, int6
 int expert_rows_blocks(int64_t P);
 cudaError_t launch_expert_rows(const int32_t* index, int64_t P, int E, int align, int64_t R, int32_t* pos, int32_t* src,
                                int32_t* start, int32_t* count, int32_t* hist, cudaStream_t st);
-cudaError_t launch_expert_gather_rows(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
-                                      const fp8rl_expert_layout& l, uint8_t* q, float* s, int num_sms, cudaStream_t st);
 cudaError_t launch_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,
                                   int64_t ldr, const fp8rl_expert_layout& l, uint16_t* out, int64_t ldo, cudaStream_t st);
 cudaError_t launch_expert_dweight(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t ldy, int64_t N,
                                   const fp8rl_expert_layout& l, float* dweight, cudaStream_t st);
 
-// quantize.cu: the gathered rows quantized 1x128 and 128x1 (l.R % 128 == 0).
-cudaError_t launch_expert_gather_dual(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
-                                      const fp8rl_expert_layout& l, uint8_t* q, float* s, uint8_t* qT, float* sT,
-                                      uint64_t timeout_ns, cudaStream_t st);
+// quantize.cu: the gathered rows quantized 1x128 and, with qT, 128x1 (l.R % 128 == 0 then).
+cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, const float* weight, const fp8rl_expert_layout& l,
+                                 uint8_t* q, float* s, uint8_t* qT, float* sT, int num_sms, uint64_t timeout_ns,
+                                 cudaStream_t st);
 
 // gemm_experts.cu: the paired-SM GEMM over the experts' row segments (aligned to 128).
 enum ExpertOp : int { EXPERT_FWD = 0, EXPERT_DGRAD = 1, EXPERT_WGRAD = 2 };

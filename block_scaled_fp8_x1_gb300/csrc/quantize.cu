@@ -339,10 +339,11 @@ __device__ __noinline__ uint4 encode4_slow(float2 x0, float2 x1, float2 x2, floa
                       e4m3x2(__fdiv_rn(x2.x, s), __fdiv_rn(x2.y, s)), e4m3x2(__fdiv_rn(x3.x, s), __fdiv_rn(x3.y, s)));
 }
 
-// 1x128 codes and scales of one thread's 8 rows (from row r0) x 8 columns (C0 ..) of column
-// block tt, q[M][ldq]; a row's group is the 16 lanes of the half-warp.
-__device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_t* q, float* s, int64_t ldq, int64_t M,
-                                               int64_t r0, int64_t tt, int C0, int lane) {
+// 1x128 codes of one thread's 8 rows x 8 columns, a row's group being the 16 lanes of the
+// half-warp: row(i, lo, hi) gets those of row i.  Lane cl returns the scale of row cl & 7, which
+// scale(s) gets before.
+template <typename SCALE, typename ROW>
+__device__ __forceinline__ void encode_rows_8x8(const uint32_t (&w)[8][4], int lane, SCALE&& scale, ROW&& row) {
     const int cl = lane & 15;
     uint32_t pm[4];   // maxima of rows (2k, 2k + 1), a half each
     #pragma unroll
@@ -363,7 +364,7 @@ __device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_
     const uint32_t pw = (ri >> 1) == 0 ? pm[0] : (ri >> 1) == 1 ? pm[1] : (ri >> 1) == 2 ? pm[2] : pm[3];
     const uint32_t mine = (ri & 1) ? (pw >> 16) : (pw & 0xFFFFu);
     const FastScale fs = fast_scale(bf16_bits_amax_to_f32(mine));
-    if (cl < 8 && r0 + cl < M) s[tt * M + r0 + cl] = fs.s;
+    scale(fs.s);
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int src = (lane & 16) | i;
@@ -380,8 +381,17 @@ __device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_
             lo = v.x | (v.y << 16);
             hi = v.z | (v.w << 16);
         }
-        if (r0 + i < M) stg_v2(q + (r0 + i) * ldq + tt * 128 + C0, lo, hi);
+        row(i, lo, hi);
     }
+}
+
+// 1x128 codes and scales of one thread's 8 rows (from row r0) x 8 columns (C0 ..) of column
+// block tt, q[M][ldq].
+__device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_t* q, float* s, int64_t ldq, int64_t M,
+                                               int64_t r0, int64_t tt, int C0, int lane) {
+    const int cl = lane & 15;
+    encode_rows_8x8(w, lane, [&](float sc) { if (cl < 8 && r0 + cl < M) s[tt * M + r0 + cl] = sc; },
+                    [&](int i, uint32_t lo, uint32_t hi) { if (r0 + i < M) stg_v2(q + (r0 + i) * ldq + tt * 128 + C0, lo, hi); });
 }
 
 // rstd of every row for PRO_RMSNORM_G: one warp per row.  The squares are summed in
@@ -494,8 +504,6 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         }
     };
 
-    // who requests tiles: thread 0, or all of warp 0 with four gathered rows a lane
-    const bool issuer = PRO == PRO_GATHER ? warp == 0 : tid == 0;
     if (tid == 0) {
         for (int st = 0; st < STAGES; ++st) mbar_init(smem_u32(&full_bar[st]), 1);
         abort_flag = 0;
@@ -513,16 +521,6 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         const int64_t k0 = tt * 128, m0 = pnl * 128;
         const uint32_t bar = smem_u32(&full_bar[st]);
         uint8_t* dst = stages + st * PS::STAGE_BYTES;
-        if (PRO == PRO_GATHER) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, PS::STAGE_BYTES);
-            __syncwarp();
-            const int4 p = __ldg(reinterpret_cast<const int4*>(a.src + m0) + lane);
-            const int64_t pairs = a.x_rows * a.k;
-            // a row without a source is read from row 0 and masked after the copy
-            auto row = [&](int v) { return v >= 0 && v < pairs ? v / a.k : 0; };
-            tma_gather4(smem_u32(dst) + 1024u * lane, &tmx, bar, (int)k0, make_int4(row(p.x), row(p.y), row(p.z), row(p.w)));
-            return;
-        }
         if (part != 2) mbar_arrive_expect_tx(bar, PS::STAGE_BYTES);
         if (PRO == PRO_DEQUANT) {
             // the code tile and the 128 row scales of its column block (one bulk copy:
@@ -549,10 +547,59 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         }
     };
     int issued = 0;
-    if (issuer)
+    // GATHER: every thread copies its own 8 rows x 16 bytes of a tile by cp.async and reads them
+    // back itself, so neither copy nor wait needs the other threads.  Lane cl holds what concerns
+    // row R0 + (cl & 7) of its half: the row of x (-1: none, zeros), looked up an item before it is
+    // requested, and the factors of the items in flight.
+    int gather_row = -1;
+    float gather_next = 0.0f, gather_f[2] = {0.0f, 0.0f};
+    // panel and tile of the item that gather_row is for, advanced without the divisions of tile_at
+    const int step_panel = (int)(gridDim.x / ntiles), step_tile = (int)(gridDim.x - step_panel * ntiles);
+    int gather_panel = (int)(blockIdx.x / ntiles), gather_tile = (int)(blockIdx.x - gather_panel * ntiles);
+    auto advance = [&](int& panel, int& tile) {
+        panel += step_panel;
+        tile += step_tile;
+        if (tile >= ntiles) {
+            tile -= (int)ntiles;
+            ++panel;
+        }
+    };
+    auto gather_find = [&](int it) {
+        gather_row = -1;
+        gather_next = 0.0f;
+        if (it >= total) return;
+        const int p = __ldg(a.src + (int64_t)gather_panel * 128 + R0 + (cl & 7));
+        if (p < 0 || p >= a.x_rows * a.k) return;
+        gather_row = p / a.k;
+        gather_next = a.weight ? __ldg(a.weight + p) : 1.0f;
+    };
+    auto gather_issue = [&](int it) {
+        const uint32_t dst = smem_u32(stages + (it % STAGES) * PS::STAGE_BYTES) + R0 * 256 + C0 * 2;
+        const uint16_t* col = a.x + gather_tile * 128 + C0;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = __shfl_sync(0xffffffffu, gather_row, (lane & 16) | i);
+            cp_async_16(dst + 256 * i, r < 0 ? a.x : col + (int64_t)r * a.ldx, r < 0 ? 0u : 16u);
+        }
+        cp_async_commit();
+        gather_f[1] = gather_f[0];
+        gather_f[0] = gather_next;
+        advance(gather_panel, gather_tile);
+        gather_find(it + 1);
+    };
+    if (PRO == PRO_GATHER) {
+        static_assert(PRO != PRO_GATHER || STAGES == 2, "the factors of two items in flight");
+        gather_find(0);
+        for (; issued < STAGES; ++issued) gather_issue(issued);
+    } else if (tid == 0) {
         for (; issued < STAGES && issued < total; ++issued) issue(issued);
+    }
     // every thread waits for item `it`; the decision to stop is made block-wide
     auto wait_item = [&](int it) -> bool {
+        if (PRO == PRO_GATHER) {
+            cp_async_wait_group<STAGES - 1>();
+            return true;
+        }
         const bool got = mbar_wait(smem_u32(&full_bar[it % STAGES]), (it / STAGES) & 1, a.timeout_ns, &abort_flag);
         return !__syncthreads_or(got ? 0 : 1);
     };
@@ -626,28 +673,23 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         const int64_t m = pnl * 128 + R0 + (cl & 7);
         return m < a.M ? __ldg(a.xs + (tt + (cl < 8 ? 0 : ntiles / 2)) * a.M + m) : 0.0f;
     };
-    // GATHER: lane cl holds the factor of row R0 + (cl & 7) of its half, likewise, and whether
-    // the row has a source
-    auto row_factor = [&](int it) {
-        int64_t pnl, tt;
-        tile_at(it, pnl, tt);
-        const int p = __ldg(a.src + pnl * 128 + R0 + (cl & 7));
-        const bool has = p >= 0 && p < a.x_rows * a.k;
-        return make_float2(!has ? 0.0f : a.weight ? __ldg(a.weight + p) : 1.0f, has ? 1.0f : 0.0f);
-    };
+    int at_panel = (int)(blockIdx.x / ntiles), at_tile = (int)(blockIdx.x - at_panel * ntiles);   // GATHER: of `item`
     float ck_next = 0.0f;
-    float2 rf_next = make_float2(0.0f, 0.0f);
     if (PRO == PRO_SILU_BWD_CK && total > 0) ck_next = ckpt_scale(0);
-    if (PRO == PRO_GATHER && total > 0) rf_next = row_factor(0);
     for (; ok && item < total; ++item) {
         const float ck_scale = ck_next;
-        const float2 rf = rf_next;
+        const float gather_w = gather_f[1];      // of this item (the next one's is gather_f[0])
         if (PRO == PRO_SILU_BWD_CK && item + 1 < total) ck_next = ckpt_scale(item + 1);
-        if (PRO == PRO_GATHER && item + 1 < total) rf_next = row_factor(item + 1);
         ok = wait_item(item);
         if (!ok) break;
         int64_t panel, t;
-        tile_at(item, panel, t);
+        if (PRO == PRO_GATHER) {
+            panel = at_panel;
+            t = at_tile;
+            advance(at_panel, at_tile);
+        } else {
+            tile_at(item, panel, t);
+        }
         const int64_t m0 = panel * 128;
         uint8_t* const stage = stages + (item % STAGES) * PS::STAGE_BYTES;
         // Quantize one output tile, column block tt, from this thread's BF16 words w (8 rows
@@ -694,7 +736,9 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             // double the registers and halve the CTAs per SM
             auto xrow = [&](int i, int j) { return make_float2(bf16_lo(w[i][j]), bf16_hi(w[i][j])); };
             __syncthreads();                                  // stage consumed, column maxima published
-            if (issuer && issued < total) {
+            if (PRO == PRO_GATHER) {
+                gather_issue(issued++);
+            } else if (tid == 0 && issued < total) {
                 if (refill == 1) issue(issued++);
                 else if (refill == 2) issue(issued, 1);
             }
@@ -916,15 +960,14 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             for (int i = 0; i < 8; ++i)   // rows past M (TMA zero fill) are never stored
                 rg[i] = (PRO == PRO_RMSNORM_G && m0 + R0 + i < a.M) ? __ldg(a.rstd_out + m0 + R0 + i) : 0.0f;
             rows_from_smem<PRO == PRO_GATHER ? PRO_COPY : PRO>(stage, a, t * 128, R0, C0, s_rstd, rg, w);
-            if (PRO == PRO_GATHER) {
+            if (PRO == PRO_GATHER && a.weight) {
                 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float f = __shfl_sync(0xffffffffu, rf.x, (lane & 16) | i);
-                    const bool has = __shfl_sync(0xffffffffu, rf.y, (lane & 16) | i) != 0.0f;
+                    const float f = __shfl_sync(0xffffffffu, gather_w, (lane & 16) | i);
                     #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (a.weight) w[i][j] = pack_bf16x2(bf16_lo(w[i][j]) * f, bf16_hi(w[i][j]) * f);
-                        if (!has) w[i][j] = 0u;
+                        const float2 y = __fmul2_rn(make_float2(bf16_lo(w[i][j]), bf16_hi(w[i][j])), make_float2(f, f));
+                        w[i][j] = pack_bf16x2(y.x, y.y);
                     }
                 }
             }
@@ -933,7 +976,9 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             quantize_tile(w, t, smem_u32(stages + PS::COLQ_OFF) + (uint32_t)(item & 1) * (128u * 128u), 1);
         }
     }
-    if (tid == 0) {
+    if (PRO == PRO_GATHER) {
+        cp_async_wait_all();
+    } else if (tid == 0) {
         // after an abort: let every issued copy land before the CTA exits
         for (int j = item; j < issued; ++j) {
             volatile int no_abort = 0;
@@ -943,6 +988,96 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
     if (PRO == PRO_RMSNORM) {
         // Keep this CTA's partial sums alive until every peer has read them.
         cg::this_cluster().sync();
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Rows of x quantized 1x128 and written to the rows of their pairs: row t of x to rows pos[t][0 .. k)
+// of the result, each times its pair's weight where one is given.  Token by token, so that a row is
+// read once however many experts it goes to and, without weights, encoded once: a copy costs its
+// stores.  (Row by row of the result the same work took 163 us at 65536 pairs x 4096: the 67 MB of x
+// come back from HBM for most experts, between the codes that are written, and every copy is encoded
+// again.)  A warp takes 16 rows x 128 columns at a time in the panel kernels' thread layout; the
+// scales of a row go to places of their own, 4 bytes each, which L2 puts together.
+// Rows of the result without a pair are zeroed by the warps as they finish.
+// ------------------------------------------------------------------------------------
+template <bool WEIGHTED>
+__global__ void __launch_bounds__(128) k_scatter_rows(const PanelArgs a, const int32_t* __restrict__ pos) {
+    const int lane = threadIdx.x & 31, half = lane >> 4, cl = lane & 15;
+    const int R0 = 8 * half, C0 = 8 * cl;
+    const int ntiles = (int)(a.K / 128);
+    const int64_t nrb = (a.x_rows + 15) / 16;
+    const int64_t first = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), step = (int64_t)gridDim.x * 4;
+    int64_t rb = first / ntiles;
+    int ct = (int)(first - rb * ntiles);
+    const int64_t d_rb = step / ntiles;
+    const int d_ct = (int)(step - d_rb * ntiles);
+    while (rb < nrb) {
+        const int64_t t0 = rb * 16 + R0;
+        const int64_t mine = t0 + (cl & 7);             // the token whose places this lane holds
+        const bool has = mine < a.x_rows;
+        uint32_t w[8][4];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (t0 + i < a.x_rows) v = ldg_nc_v4(a.x + (t0 + i) * a.ldx + ct * 128 + C0);
+            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+        }
+        auto place = [&](int j) {
+            const int r = has ? __ldg(pos + mine * a.k + j) : -1;
+            return r >= 0 && r < a.M ? r : -1;
+        };
+        uint8_t* const q = a.q + ct * 128 + C0;
+        float* const s = a.s + (int64_t)ct * a.M;
+        if constexpr (!WEIGHTED) {
+            uint32_t lo[8], hi[8];
+            float sc = 0.0f;
+            encode_rows_8x8(w, lane, [&](float v) { sc = v; }, [&](int i, uint32_t l, uint32_t h) { lo[i] = l; hi[i] = h; });
+            for (int j = 0; j < a.k; ++j) {
+                const int r = place(j);
+                if (r >= 0 && cl < 8) s[r] = sc;
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int ri = __shfl_sync(0xffffffffu, r, (lane & 16) | i);
+                    if (ri >= 0) stg_v2(q + (int64_t)ri * a.K, lo[i], hi[i]);
+                }
+            }
+        } else {
+            for (int j = 0; j < a.k; ++j) {
+                const int r = place(j);
+                const float f = r >= 0 ? __ldg(a.weight + mine * a.k + j) : 0.0f;
+                uint32_t y[8][4];
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float g = __shfl_sync(0xffffffffu, f, (lane & 16) | i);
+                    #pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 v = __fmul2_rn(make_float2(bf16_lo(w[i][c]), bf16_hi(w[i][c])), make_float2(g, g));
+                        y[i][c] = pack_bf16x2(v.x, v.y);
+                    }
+                }
+                encode_rows_8x8(y, lane, [&](float v) { if (r >= 0 && cl < 8) s[r] = v; },
+                                [&](int i, uint32_t l, uint32_t h) {
+                                    const int ri = __shfl_sync(0xffffffffu, r, (lane & 16) | i);
+                                    if (ri >= 0) stg_v2(q + (int64_t)ri * a.K, l, h);
+                                });
+            }
+        }
+        rb += d_rb;
+        ct += d_ct;
+        if (ct >= ntiles) {
+            ct -= ntiles;
+            ++rb;
+        }
+    }
+    // rows of no pair
+    for (int64_t r0 = first * 32; r0 < a.M; r0 += step * 32) {
+        const int p = r0 + lane < a.M ? __ldg(a.src + r0 + lane) : 0;
+        for (uint32_t none = __ballot_sync(0xffffffffu, p < 0 || p >= a.x_rows * a.k); none; none &= none - 1) {
+            const int64_t r = r0 + __ffs(none) - 1;
+            for (int64_t c = lane * 16; c < a.K; c += 512) *reinterpret_cast<uint4*>(a.q + r * a.K + c) = make_uint4(0, 0, 0, 0);
+            for (int c = lane; c < ntiles; c += 32) a.s[(int64_t)c * a.M + r] = 0.0f;
+        }
     }
 }
 
@@ -1189,14 +1324,13 @@ cudaError_t launch_quant_1x128(const uint16_t* x, int64_t M, int64_t K, int64_t 
     return cudaGetLastError();
 }
 
-// 2-D tensor map of a BF16 matrix [rows][cols] (row stride ld elements), box_rows x 128 boxes.
-static cudaError_t tmap_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
-                             unsigned box_rows = 128) {
+// 2-D tensor map of a BF16 matrix [rows][cols] (row stride ld elements), 128x128 boxes.
+static cudaError_t tmap_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return cudaErrorNotSupported;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {128u, box_rows};
+    cuuint32_t box[2] = {128u, 128u};
     cuuint32_t es[2] = {1u, 1u};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -1223,8 +1357,7 @@ static cudaError_t launch_panel_t(const PanelArgs& a, int64_t in_cols, int clust
     CUtensorMap tm, tm2;
     constexpr bool pair = PRO == PRO_SILU_BWD || PRO == PRO_SILU_BWD_CK;
     cudaError_t e = PRO == PRO_DEQUANT || PRO == PRO_SILU_BWD_CK ? tmap_u8(&tm, a.x, a.M, in_cols)
-                    : PRO == PRO_GATHER ? tmap_bf16(&tm, a.x, a.x_rows, in_cols, a.ldx, 1)
-                                        : tmap_bf16(&tm, a.x, a.M, in_cols, a.ldx);
+                    : tmap_bf16(&tm, a.x, PRO == PRO_GATHER ? a.x_rows : a.M, in_cols, a.ldx);
     if (e != cudaSuccess) return e;
     if (pair) {
         e = tmap_bf16(&tm2, a.x2, a.M, a.K / 2, a.K / 2);
@@ -1281,15 +1414,20 @@ cudaError_t launch_quant_dual(const uint16_t* x, int64_t M, int64_t K, int64_t l
     return launch_panel_t<PRO_COPY, false, true>(a, K, 0, st);
 }
 
-// rows of x in expert order, each times its pair's weight, quantized 1x128 and 128x1
-cudaError_t launch_expert_gather_dual(const uint16_t* x, int64_t ldx, int64_t K, const float* weight,
-                                      const fp8rl_expert_layout& l, uint8_t* q, float* s, uint8_t* qT, float* sT,
-                                      uint64_t timeout_ns, cudaStream_t st) {
+// rows of x in expert order, each times its pair's weight, quantized 1x128 and (qT) 128x1
+cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, const float* weight, const fp8rl_expert_layout& l,
+                                 uint8_t* q, float* s, uint8_t* qT, float* sT, int num_sms, uint64_t timeout_ns,
+                                 cudaStream_t st) {
     PanelArgs a = {};
     a.x = x; a.ldx = ldx; a.M = l.R; a.K = K; a.q = q; a.s = s; a.qT = qT; a.sT = sT;
     a.src = l.src; a.weight = weight; a.x_rows = l.T; a.k = (int)l.k;
     a.timeout_ns = timeout_ns;
-    return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
+    if (qT) return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
+    const int64_t items = (l.T + 15) / 16 * (K / 128);
+    const int64_t blocks = std::min<int64_t>((items + 3) / 4, (int64_t)num_sms * 8);
+    if (weight) k_scatter_rows<true><<<(unsigned)blocks, 128, 0, st>>>(a, l.pos);
+    else k_scatter_rows<false><<<(unsigned)blocks, 128, 0, st>>>(a, l.pos);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_silu_mul_quant(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s,
