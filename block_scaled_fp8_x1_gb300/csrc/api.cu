@@ -1249,8 +1249,10 @@ fp8rl_status run_decode_experts(const ExpertArgs& g, const fp8rl_expert_layout& 
     const int64_t P = l.T * l.k, tiles = g.N / 128, nkb = g.K / 128;
     const int tokens = expert_decode_tokens(P, l.E);
     const int64_t units = std::min(l.E, P) + P / tokens;    // sum of ceil(count / tokens) is no more
-    const int splits = expert_decode_splits(units, tiles, nkb, num_sms);
-    if (units * tiles > (int64_t(1) << 30) / splits) return FP8RL_ERR_SHAPE;
+    if (units > (int64_t(1) << 30) / tiles) return FP8RL_ERR_SHAPE;
+    const int64_t items = units * tiles;
+    const int splits = expert_decode_splits(items, nkb, num_sms);
+    const int clusters = (int)(splits > 1 ? items : std::min<int64_t>(items, 2 * (int64_t)num_sms));
     CUtensorMap tw, tx;
     fp8rl_status e = make_tmap(&tw, g.b, l.E * g.N, g.K, g.K, 128);
     if (e != FP8RL_OK) return e;
@@ -1267,7 +1269,7 @@ fp8rl_status run_decode_experts(const ExpertArgs& g, const fp8rl_expert_layout& 
     p.y = g.c;
     p.ldy = g.N;
     p.timeout_ns = g_timeout_ns.load();
-    return cuda_status(launch_decode_experts(tw, tx, p, tokens, units, splits, st));
+    return cuda_status(launch_decode_experts(tw, tx, p, tokens, clusters, splits, st));
 }
 
 fp8rl_status gemm_experts(ExpertOp op, const ExpertArgs& g, const fp8rl_expert_layout* rows, cudaStream_t st) {

@@ -6,13 +6,15 @@
 // experts that have rows cross HBM once and bound the time, as in decode.cu, whose tile this is
 // (A = 128 weight rows x 128, B = the activations of up to MP rows).
 //
-// Work: (unit, weight tile), a unit being up to MP rows of one expert, in a cluster of S CTAs that
-// split the reduction and add their FP32 sums in rank order through distributed shared memory.  The
-// host knows only how many units there can be; a cluster finds its own from the counts (a warp's
-// running sum over 32 experts at a time), and those past the last leave at once.  A CTA takes
-// half of an SM's shared memory and registers, so one CTA's start and end are under another's
-// copies, and the SMs pick up clusters as they become free.
-// Rows of the segment start anywhere: the copy of X has the rows of the next expert behind the
+// Work: items (unit, weight tile), a unit being up to MP rows of one expert.  A CTA takes half of an
+// SM's shared memory and registers.  Two CTAs an SM walk the items with one continuous copy / MMA /
+// epilogue pipeline each: a CTA's start (about 5 us from launch to its first sums: the counts,
+// tensor memory, the first copies) is paid once, not per item (1472 items of 11 K-blocks one a CTA:
+// 45 us, HIST).  Where the items are fewer than the SMs, a cluster of S CTAs shares each item's
+// reduction instead and adds its FP32 sums in rank order through distributed shared memory.
+// The host knows only how many units there can be; each CTA sums up the experts' units from the
+// counts when it starts.
+// Rows of a segment start anywhere: the copy of X has the rows of the next expert behind the
 // unit's, which give columns that are not stored.
 // Every mbarrier wait is bounded (FP8RL_ERR_DEVICE_TIMEOUT).
 #include <algorithm>
@@ -41,8 +43,9 @@ struct XDecodeCfg {
     static constexpr size_t STAGE_BYTES = (size_t)STAGES * (W_BYTES + X_BYTES);
     static_assert((size_t)MP * 128 * 4 <= STAGE_BYTES, "the reduction buffer reuses the stage ring");
     static constexpr int NBARS = 2 * STAGES + 2 * NB + 3 * NSC + 1;
-    static constexpr size_t BYTES = 1024 + STAGE_BYTES + (size_t)NSC * (SLOT + MP) * 4 + NBARS * 8 + 32;
-    static_assert(COLS <= 256 && BYTES <= 113 * 1024, "two CTAs an SM");
+    static constexpr size_t FIXED = 1024 + STAGE_BYTES + (size_t)NSC * (SLOT + MP) * 4 + NBARS * 8 + 16 + 16 * 4;
+    static size_t bytes(int E) { return FIXED + (2 * (size_t)E + 1) * 4; }
+    static_assert(COLS <= 256 && FIXED + (2 * kMaxExperts + 1) * 4 <= 113 * 1024, "two CTAs an SM");
 };
 
 }  // namespace
@@ -73,17 +76,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t* drain_bar = sempty_bar + NSC;     // [1] MMA completion at exit
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* s_unit = reinterpret_cast<int*>(tmem_slot + 2);                       // expert, first row, rows
+    int* s_warp = reinterpret_cast<int*>(tmem_slot + 4);                       // [12] units of a warp's experts
+    int* s_units = s_warp + 16;                                                // [E + 1] units of the experts before
+    int* s_start = s_units + p.E + 1;                                          // [E]
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int S = (int)cluster_nctarank();
     const int rank = (int)cluster_ctarank();
-    const int unit = (int)cluster_idx() / p.tiles;
-    const int tile = (int)cluster_idx() - unit * p.tiles;
     const int kb0 = (int)(((int64_t)rank * p.nkb) / S);
     const int kb1 = (int)(((int64_t)(rank + 1) * p.nkb) / S);
-    const int nk = kb1 - kb0;                   // K-blocks of this CTA (>= 1)
+    const int nk = kb1 - kb0;                   // K-blocks of an item for this CTA (>= 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -105,188 +108,228 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
     }
-    if (warp == 2) {
-        // unit -> expert: units before each expert by a running sum over 32 experts at a time
-        int before = 0;
-        bool found = false;
-        for (int e0 = 0; e0 < p.E && !found; e0 += 32) {
-            const int e = e0 + lane;
-            const int c = e < p.E ? max(0, __ldg(p.count + e)) : 0;
-            const int n = (c + MP - 1) / MP;
-            int scan = n;
-            #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, scan, o);
-                if (lane >= o) scan += v;
-            }
-            const int i = unit - (before + scan - n);     // unit within this expert
-            const bool here = i >= 0 && i < n;
-            if (here) {
-                s_unit[0] = e;
-                s_unit[1] = __ldg(p.start + e) + i * MP;
-                s_unit[2] = min(MP, c - i * MP);
-            }
-            found = __any_sync(0xffffffffu, here);
-            before += __shfl_sync(0xffffffffu, scan, 31);
-        }
-        if (!found && lane == 0) s_unit[2] = 0;
-    }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::COLS);
         tmem_relinquish();
     }
+    grid_dependency_begin();
+    // units of the experts before each expert
+    int carry = 0;
+    for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+        const int e = e0 + (int)threadIdx.x;
+        const int n = e < p.E ? (max(0, __ldg(p.count + e)) + MP - 1) / MP : 0;
+        if (e < p.E) s_start[e] = __ldg(p.start + e);
+        int scan = n;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+        }
+        if (lane == 31) s_warp[warp] = scan;
+        __syncthreads();
+        int total = 0;
+        #pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) scan += s_warp[i];
+            total += s_warp[i];
+        }
+        if (e < p.E) s_units[e] = carry + scan - n;
+        carry += total;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) s_units[p.E] = carry;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int expert = s_unit[0], row0 = s_unit[1];
-    int rows = s_unit[2];                       // 0: no unit of this number
-    if (rows > 0 && (row0 < 0 || row0 + (int64_t)rows > p.R)) {
-        record_status(FP8RL_ERR_DEVICE_BOUNDS); // starts and counts that do not fit the rows
-        rows = 0;
-    }
-    bool ok = rows > 0;
+    // items of this CTA: first, first + step, ... (one at most where the reduction is split)
+    const int items = carry * p.tiles;
+    const int first = (int)cluster_idx(), step = (int)cluster_count();
+    bool ok = true;
+    // Item -> expert, weight tile and rows
+    struct Item {
+        int expert, tile, row0, rows;
+    };
+    auto item_at = [&](int item) {
+        Item t;
+        const int unit = (int)((uint32_t)item / (uint32_t)p.tiles);
+        t.tile = item - unit * p.tiles;
+        int e = 0, above = p.E;          // s_units[e] <= unit < s_units[above]
+        while (above - e > 1) {
+            const int mid = (e + above) >> 1;
+            if (s_units[mid] <= unit) e = mid;
+            else above = mid;
+        }
+        t.expert = e;
+        const int before = (unit - s_units[e]) * MP;
+        t.row0 = s_start[e] + before;
+        t.rows = min(MP, max(0, __ldg(p.count + e)) - before);
+        // starts and counts that do not fit the rows: nothing is read or written there
+        if (t.row0 < 0 || (int64_t)t.row0 + t.rows > p.R) {
+            record_status(FP8RL_ERR_DEVICE_BOUNDS);
+            t.row0 = t.rows = 0;
+        }
+        return t;
+    };
 
     if (warp < 4) {
-        if (warp == 0 && ok) {
+        if (warp == 0) {
             // ------------------------------------------------------------ copies
             const uint64_t pol_w = l2_policy_evict_first();   // each weight byte is read once
             const uint64_t pol_x = l2_policy_evict_last();    // every tile reads the activation
             constexpr uint32_t TX = C::W_BYTES + C::X_BYTES;
-            const int wy = (expert * p.tiles + tile) * 128;
-            const float* swt = p.sw + ((int64_t)expert * p.tiles + tile) * p.nkb;
-            int i = 0;
-            for (; i < nk; ++i) {
-                const int kb = kb0 + i;
-                const uint32_t s = (uint32_t)i % STAGES;
-                if (!mbar_wait(smem_u32(&empty_bar[s]), ((i / STAGES) & 1) ^ 1, p.timeout_ns, abort_flag)) {
-                    ok = false;
-                    break;
+            uint32_t it = 0;
+            for (int item = first; ok && item < items; item += step) {
+                const Item t = item_at(item);
+                const int wy = (t.expert * p.tiles + t.tile) * 128;
+                const float* swt = p.sw + ((int64_t)t.expert * p.tiles + t.tile) * p.nkb;
+                for (int i = 0; i < nk; ++i, ++it) {
+                    const int kb = kb0 + i;
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait(smem_u32(&empty_bar[s]), ((it / STAGES) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one_sync()) {
+                        mbar_arrive_expect_tx(smem_u32(&full_bar[s]), TX);
+                        tma_load_2d(smem_u32(sW + s * C::W_BYTES), &tmW, smem_u32(&full_bar[s]), kb * 128, wy, pol_w);
+                        tma_load_2d(smem_u32(sX + s * C::X_BYTES), &tmX, smem_u32(&full_bar[s]), kb * 128, t.row0, pol_x);
+                    }
+                    __syncwarp();
+                    // this K-block's scales: sx(kb, r) of the unit's rows (zero behind them) and
+                    // sw(tile, kb), by asynchronous copies whose landing completes the slot's barrier
+                    const uint32_t ss = it % NSC;
+                    if (!mbar_wait(smem_u32(&sempty_bar[ss]), ((it / NSC) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+                        ok = false;
+                        ++it;
+                        break;
+                    }
+                    const uint32_t slot = smem_u32(sc_ring + ss * SLOT);
+                    const float* sxk = p.sx + (int64_t)kb * p.R + t.row0;
+                    #pragma unroll
+                    for (int c = lane; c < MP; c += 32) {
+                        const bool v = c < t.rows;
+                        cp_async_4(slot + 4u * (uint32_t)c, v ? sxk + c : p.sx, v ? 4u : 0u);
+                    }
+                    if (lane == 0) cp_async_4(slot + 4u * MP, swt + kb, 4u);
+                    cp_async_arrive(smem_u32(&sfull_bar[ss]));
                 }
-                if (elect_one_sync()) {
-                    mbar_arrive_expect_tx(smem_u32(&full_bar[s]), TX);
-                    tma_load_2d(smem_u32(sW + s * C::W_BYTES), &tmW, smem_u32(&full_bar[s]), kb * 128, wy, pol_w);
-                    tma_load_2d(smem_u32(sX + s * C::X_BYTES), &tmX, smem_u32(&full_bar[s]), kb * 128, row0, pol_x);
-                }
-                __syncwarp();
-                // this K-block's scales: sx(kb, r) of the unit's rows (zero behind them) and
-                // sw(tile, kb), by asynchronous copies whose landing completes the slot's barrier
-                const uint32_t ss = (uint32_t)i % NSC;
-                if (!mbar_wait(smem_u32(&sempty_bar[ss]), ((i / NSC) & 1) ^ 1, p.timeout_ns, abort_flag)) {
-                    ok = false;
-                    ++i;
-                    break;
-                }
-                const uint32_t slot = smem_u32(sc_ring + ss * SLOT);
-                const float* sxk = p.sx + (int64_t)kb * p.R + row0;
-                #pragma unroll
-                for (int c = lane; c < MP; c += 32) {
-                    const bool v = c < rows;
-                    cp_async_4(slot + 4u * (uint32_t)c, v ? sxk + c : sxk, v ? 4u : 0u);
-                }
-                if (lane == 0) cp_async_4(slot + 4u * MP, swt + kb, 4u);
-                cp_async_arrive(smem_u32(&sfull_bar[ss]));
             }
             // Drain: every issued copy lands before the stage memory is reused or freed.
             cp_async_wait_all();
             volatile int no_abort = 0;
-            for (int j = i > STAGES ? i - STAGES : 0; j < i; ++j)
+            const uint32_t n_out = it < (uint32_t)STAGES ? it : (uint32_t)STAGES;
+            for (uint32_t j = it - n_out; j < it; ++j)
                 mbar_wait(smem_u32(&full_bar[j % STAGES]), (j / STAGES) & 1, p.timeout_ns, &no_abort);
-        } else if (warp == 1 && ok) {
+        } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             const uint32_t w_base = smem_u32(sW), x_base = smem_u32(sX);
-            for (int i = 0; i < nk; ++i) {
-                const uint32_t ts = (uint32_t)i % NB;
-                const uint32_t s = (uint32_t)i % STAGES;
-                if (!mbar_wait(smem_u32(&tempty_bar[ts]), ((i / NB) & 1) ^ 1, p.timeout_ns, abort_flag) ||
-                    !mbar_wait(smem_u32(&full_bar[s]), (i / STAGES) & 1, p.timeout_ns, abort_flag)) {
-                    ok = false;
-                    break;
+            uint32_t it = 0;
+            for (int item = first; ok && item < items; item += step) {
+                for (int i = 0; i < nk; ++i, ++it) {
+                    const uint32_t ts = it % NB;
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait(smem_u32(&tempty_bar[ts]), ((it / NB) & 1) ^ 1, p.timeout_ns, abort_flag) ||
+                        !mbar_wait(smem_u32(&full_bar[s]), (it / STAGES) & 1, p.timeout_ns, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + ts * MP;
+                    const uint64_t da = sdesc_kmajor_sw128(w_base + s * C::W_BYTES);
+                    const uint64_t db = sdesc_kmajor_sw128(x_base + s * C::X_BYTES);
+                    if (elect_one_sync()) {
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k)   // 32-byte steps inside the 128-byte rows
+                            mma_f8(d, da + 2 * k, db + 2 * k, IDESC, k > 0 ? 1u : 0u);
+                        mma_commit(smem_u32(&empty_bar[s]));
+                        mma_commit(smem_u32(&tfull_bar[ts]));
+                    }
+                    __syncwarp();
                 }
-                tc_fence_after();
-                const uint32_t d = tmem_base + ts * MP;
-                const uint64_t da = sdesc_kmajor_sw128(w_base + s * C::W_BYTES);
-                const uint64_t db = sdesc_kmajor_sw128(x_base + s * C::X_BYTES);
-                if (elect_one_sync()) {
-                    #pragma unroll
-                    for (int k = 0; k < 4; ++k)   // 32-byte steps inside the 128-byte rows
-                        mma_f8(d, da + 2 * k, db + 2 * k, IDESC, k > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&empty_bar[s]));
-                    mma_commit(smem_u32(&tfull_bar[ts]));
-                }
-                __syncwarp();
             }
             if (elect_one_sync()) mma_commit(smem_u32(drain_bar));
             __syncwarp();
             volatile int no_abort = 0;
             mbar_wait(smem_u32(drain_bar), 0, p.timeout_ns, &no_abort);
-        } else if (warp == 2 && ok) {
+        } else if (warp == 2) {
             // ------------------------------------------------------------ scale combiner
             // per K-block, once for all epilogue threads: comb[r] = sx(kb, r) * sw(tile, kb)
-            for (int i = 0; i < nk; ++i) {
-                const uint32_t ss = (uint32_t)i % NSC;
-                if (!mbar_wait(smem_u32(&sfull_bar[ss]), (i / NSC) & 1, p.timeout_ns, abort_flag)) break;
-                const float* src = sc_ring + ss * SLOT;
-                const float fw = src[MP];
-                #pragma unroll
-                for (int c = lane; c < MP; c += 32) comb[ss * MP + c] = src[c] * fw;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&cfull_bar[ss]));
+            uint32_t it = 0;
+            for (int item = first; ok && item < items; item += step) {
+                for (int i = 0; i < nk; ++i, ++it) {
+                    const uint32_t ss = it % NSC;
+                    if (!mbar_wait(smem_u32(&sfull_bar[ss]), (it / NSC) & 1, p.timeout_ns, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const float* src = sc_ring + ss * SLOT;
+                    const float fw = src[MP];
+                    #pragma unroll
+                    for (int c = lane; c < MP; c += 32) comb[ss * MP + c] = src[c] * fw;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&cfull_bar[ss]));
+                }
             }
         }
-    } else if (ok) {
+    } else {
         // ------------------------------------------------------------ epilogue warps
         const int quad = warp & 3;                    // TMEM lane quadrant of this warp
         const int col0 = ((warp - 4) >> 2) * CPT;     // first column (row of X) of this thread
         const int wrow = quad * 32 + lane;            // weight row within the tile
         const uint32_t tb_lane = tmem_base + ((uint32_t)(quad * 32) << 16) + col0;
-        float2 acc[CPT / 2];
-        #pragma unroll
-        for (int c = 0; c < CPT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-        for (int i = 0; i < nk; ++i) {
-            const uint32_t ts = (uint32_t)i % NB, ss = (uint32_t)i % NSC;
-            bool got = mbar_wait(smem_u32(&cfull_bar[ss]), (i / NSC) & 1, p.timeout_ns, abort_flag);
-            got = got && mbar_wait(smem_u32(&tfull_bar[ts]), (i / NB) & 1, p.timeout_ns, abort_flag);
-            ok = __all_sync(0xffffffffu, got);
+        uint32_t it = 0;
+        for (int item = first; ok && item < items; item += step) {
+            float2 acc[CPT / 2];
+            #pragma unroll
+            for (int c = 0; c < CPT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < nk; ++i, ++it) {
+                const uint32_t ts = it % NB, ss = it % NSC;
+                bool got = mbar_wait(smem_u32(&cfull_bar[ss]), (it / NSC) & 1, p.timeout_ns, abort_flag);
+                got = got && mbar_wait(smem_u32(&tfull_bar[ts]), (it / NB) & 1, p.timeout_ns, abort_flag);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                tc_fence_after();
+                const float* sc = comb + ss * MP + col0;
+                uint32_t r[LW];
+                static_assert(CPT == LW, "one TMEM load a K-block");
+                tmem_ld_cols(tb_lane + ts * MP, r);
+                tmem_ld_wait(r);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[ts]));
+                #pragma unroll
+                for (int j = 0; j < LW; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(sc + j);
+                    acc[j / 2] = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                            make_float2(f.x, f.y), acc[j / 2]);
+                    acc[j / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                                make_float2(f.z, f.w), acc[j / 2 + 1]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sempty_bar[ss]));
+            }
             if (!ok) break;
-            tc_fence_after();
-            const float* sc = comb + ss * MP + col0;
-            uint32_t r[LW];
-            static_assert(CPT == LW, "one TMEM load a K-block");
-            tmem_ld_cols(tb_lane + ts * MP, r);
-            tmem_ld_wait(r);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[ts]));
-            #pragma unroll
-            for (int j = 0; j < LW; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(sc + j);
-                acc[j / 2] = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                        make_float2(f.x, f.y), acc[j / 2]);
-                acc[j / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
-                                            make_float2(f.z, f.w), acc[j / 2 + 1]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sempty_bar[ss]));
-        }
-        if (ok && S == 1) {
-            // the whole reduction is here: BF16 straight from registers, row by row (a warp's 32
-            // weight rows of one token are 64 contiguous bytes)
-            uint16_t* yt = p.y + (int64_t)row0 * p.ldy + tile * 128 + wrow;
-            #pragma unroll
-            for (int c = 0; c < CPT / 2; ++c) {
-                const int t0 = col0 + 2 * c;
-                const uint32_t pk = pack_bf16x2(acc[c].x, acc[c].y);
-                if (t0 < rows) yt[(int64_t)t0 * p.ldy] = (uint16_t)(pk & 0xFFFFu);
-                if (t0 + 1 < rows) yt[(int64_t)(t0 + 1) * p.ldy] = (uint16_t)(pk >> 16);
-            }
-        } else if (ok) {
-            // every MMA of this CTA has completed and every tile copy was consumed by one, so the
-            // stage ring is free: park this CTA's sums as red[row of X][weight row]
-            #pragma unroll
-            for (int c = 0; c < CPT / 2; ++c) {
-                red[(col0 + 2 * c) * 128 + wrow] = acc[c].x;
-                red[(col0 + 2 * c + 1) * 128 + wrow] = acc[c].y;
+            if (S == 1) {
+                // the whole reduction is here: BF16 straight from registers, row by row (a warp's 32
+                // weight rows of one token are 64 contiguous bytes)
+                const Item t = item_at(item);
+                uint16_t* yt = p.y + (int64_t)t.row0 * p.ldy + t.tile * 128 + wrow;
+                #pragma unroll
+                for (int c = 0; c < CPT / 2; ++c) {
+                    const int t0 = col0 + 2 * c;
+                    const uint32_t pk = pack_bf16x2(acc[c].x, acc[c].y);
+                    if (t0 < t.rows) yt[(int64_t)t0 * p.ldy] = (uint16_t)(pk & 0xFFFFu);
+                    if (t0 + 1 < t.rows) yt[(int64_t)(t0 + 1) * p.ldy] = (uint16_t)(pk >> 16);
+                }
+            } else {
+                // every MMA of this CTA has completed and every tile copy was consumed by one, so the
+                // stage ring is free: park this CTA's sums as red[row of X][weight row]
+                #pragma unroll
+                for (int c = 0; c < CPT / 2; ++c) {
+                    red[(col0 + 2 * c) * 128 + wrow] = acc[c].x;
+                    red[(col0 + 2 * c + 1) * 128 + wrow] = acc[c].y;
+                }
             }
         }
     }
@@ -296,9 +339,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     if (S > 1) {
         cluster_sync_all();
-        if (warp >= 4 && *abort_flag == 0 && rows > 0) {
+        if (warp >= 4 && *abort_flag == 0 && first < items) {
+            const Item t = item_at(first);
             const int et = threadIdx.x - 128;                     // 0..255
-            const int n4 = rows * 32;                             // float4s of the unit's rows
+            const int n4 = t.rows * 32;                           // float4s of the unit's rows
             const int per = (n4 + S - 1) / S;
             const int e_end = min(n4, (rank + 1) * per);
             const uint32_t red_local = smem_u32(red);
@@ -314,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 uint2 o;
                 o.x = pack_bf16x2(v.x, v.y);
                 o.y = pack_bf16x2(v.z, v.w);
-                *reinterpret_cast<uint2*>(p.y + (int64_t)(row0 + tok) * p.ldy + tile * 128 + r4) = o;
+                *reinterpret_cast<uint2*>(p.y + (int64_t)(t.row0 + tok) * p.ldy + t.tile * 128 + r4) = o;
             }
         }
         cluster_sync_all();   // no CTA leaves while another still reads its shared memory
@@ -328,38 +372,43 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int MP>
-static cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertDecodeParams& p, int64_t units,
+static cudaError_t launch_t(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertDecodeParams& p, int clusters,
                             int splits, cudaStream_t st) {
     auto kern = k_decode_experts<MP>;
-    constexpr size_t smem = XDecodeCfg<MP>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)XDecodeCfg<MP>::bytes((int)kMaxExperts));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * p.tiles * splits), 1, 1);
+    cfg.gridDim = dim3((unsigned)(clusters * splits), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = XDecodeCfg<MP>::bytes(p.E);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)splits;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, tw, tx, p);
 }
 
 int expert_decode_tokens(int64_t P, int64_t E) { return P <= 16 * std::min(P, E) ? 32 : 64; }
 
-int expert_decode_splits(int64_t units, int64_t tiles, int64_t nkb, int num_sms) {
-    int64_t s = 1;
-    while (s < 8 && units * tiles * s < 4 * (int64_t)num_sms && nkb / (2 * s) >= 4) s *= 2;
-    return (int)s;
+// CTAs that share an item's reduction: as many as leave no more CTAs than fit at once (two an SM),
+// and at least 4 K-blocks each.  A second wave costs more than the split saves (88 tiles of 32
+// K-blocks: one CTA each 14.2 us, 2 12.7, 3 12.4, 4 16.3, 8 20.2; 176 tiles: 19.0, 23.9, 22.7, 26.0, 34.3).
+int expert_decode_splits(int64_t items, int64_t nkb, int num_sms) {
+    int64_t s = 2 * (int64_t)num_sms / std::max<int64_t>(items, 1);
+    s = std::min<int64_t>(s, nkb / 4);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 8));
 }
 
 cudaError_t launch_decode_experts(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertDecodeParams& p, int tokens,
-                                  int64_t units, int splits, cudaStream_t st) {
-    return tokens == 32 ? launch_t<32>(tw, tx, p, units, splits, st) : launch_t<64>(tw, tx, p, units, splits, st);
+                                  int clusters, int splits, cudaStream_t st) {
+    return tokens == 32 ? launch_t<32>(tw, tx, p, clusters, splits, st) : launch_t<64>(tw, tx, p, clusters, splits, st);
 }
 
 // Reads and clears this translation unit's device status word.  The caller has synchronized the

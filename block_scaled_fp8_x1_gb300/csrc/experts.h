@@ -65,9 +65,10 @@ struct ExpertDecodeParams {
     uint64_t timeout_ns;
 };
 int expert_decode_tokens(int64_t P, int64_t E);                    // token rows of a tile
-int expert_decode_splits(int64_t units, int64_t tiles, int64_t nkb, int num_sms);
+int expert_decode_splits(int64_t items, int64_t nkb, int num_sms);  // CTAs of a cluster
+// `clusters` of `splits` CTAs: one for every item there can be when splits > 1, else any number.
 cudaError_t launch_decode_experts(const CUtensorMap& tw, const CUtensorMap& tx, const ExpertDecodeParams& p, int tokens,
-                                  int64_t units, int splits, cudaStream_t st);
+                                  int clusters, int splits, cudaStream_t st);
 fp8rl_status read_and_clear_decode_experts_status();
 
 }  // namespace fp8rl
