@@ -1180,7 +1180,7 @@ fp8rl_status check_layout(const fp8rl_expert_layout* l, const char* needs) {
     for (const char* c = needs; *c; ++c) {
         const int32_t* p = *c == 'p' ? l->pos : *c == 's' ? l->src : *c == 'b' ? l->start : l->count;
         if (!p) return FP8RL_ERR_INVALID_ARG;
-        if (!aligned_to(p, *c == 's' ? 16 : 4)) return FP8RL_ERR_ALIGN;
+        if (!aligned_to(p, 4)) return FP8RL_ERR_ALIGN;
     }
     return FP8RL_OK;
 }
@@ -1338,7 +1338,7 @@ fp8rl_status fp8rl_expert_rows(const int32_t* index, int64_t T, int64_t k, int64
     if (T < 0 || k < 1 || E < 1) return FP8RL_ERR_INVALID_ARG;
     if (!expert_sizes(T, k, E, align)) return FP8RL_ERR_SHAPE;
     if (!start || !count || (T > 0 && (!index || !pos || !src))) return FP8RL_ERR_INVALID_ARG;
-    if (!aligned_to(index, 4) || !aligned_to(pos, 4) || !aligned16(src) || !aligned16(start) || !aligned_to(count, 4))
+    if (!aligned_to(index, 4) || !aligned_to(pos, 4) || !aligned_to(src, 4) || !aligned_to(start, 4) || !aligned_to(count, 4))
         return FP8RL_ERR_ALIGN;
     const size_t need = fp8rl_expert_rows_workspace_bytes(T, k, E);
     if (need > 0 && (!ws || ws_bytes < need)) return FP8RL_ERR_WORKSPACE;

@@ -97,7 +97,14 @@ struct XWalk {
             units = (rows + 255) / 256;
         } else {
             t.nkb = nkb;
-            while (tiles[e + 1] <= item) ++e;
+            if (tiles[e + 1] <= item) {      // tiles[e] <= item < tiles[above]
+                int above = E;
+                while (above - e > 1) {
+                    const int mid = (e + above) >> 1;
+                    if (tiles[mid] <= item) e = mid;
+                    else above = mid;
+                }
+            }
             item -= tiles[e];
             units = (start[e + 1] - start[e] + 255) / 256;
         }

@@ -770,22 +770,21 @@ def expert_rows(index: torch.Tensor, n_experts: int, align: int = 128) -> Expert
     _matrix(index, "index")
     _require(index, torch.int32, "index")
     _contig(index, "index")
-    (T, k), E, dev = index.shape, int(n_experts), index.device
+    (T, k), E, align, dev = index.shape, int(n_experts), int(align), index.device
     L = lib()
-    R = int(L.fp8rl_expert_rows_capacity(T, k, E, int(align)))
-    # one allocation: src and start 16-byte aligned, then count and pos
-    at, n = [0], E if E > 0 else 0
-    for size in (R, n + 1, n):
-        at.append(at[-1] + (size + 3) // 4 * 4)
-    buf = torch.empty(at[3] + T * k, dtype=torch.int32, device=dev)
-    src, start, count = buf[:R], buf[at[1]:at[1] + n + 1], buf[at[2]:at[2] + n]
-    pos = buf[at[3]:].view(T, k)
-    need = int(L.fp8rl_expert_rows_workspace_bytes(T, k, E))
+    R = L.fp8rl_expert_rows_capacity(T, k, E, align)
+    n = E if E > 0 else 0
+    # the four arrays in one allocation
+    buf = torch.empty(R + 2 * n + 1 + T * k, dtype=torch.int32, device=dev)
+    src, start = buf.as_strided((R,), (1,), 0), buf.as_strided((n + 1,), (1,), R)
+    count, pos = buf.as_strided((n,), (1,), R + n + 1), buf.as_strided((T, k), (k, 1), R + 2 * n + 1)
+    need = L.fp8rl_expert_rows_workspace_bytes(T, k, E)
     # a buffer of this call's own: calls may run on several streams
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    check(L.fp8rl_expert_rows(_ptr(index), T, k, E, int(align), _ptr(pos), _ptr(src), _ptr(start), _ptr(count), _ptr(ws),
-                              need, _stream(dev)), "fp8rl_expert_rows")
-    return ExpertRows(pos, src, start, count, int(align))
+    at = buf.data_ptr()
+    check(L.fp8rl_expert_rows(index.data_ptr(), T, k, E, align, at + 4 * (R + 2 * n + 1), at, at + 4 * R,
+                              at + 4 * (R + n + 1), _ptr(ws), need, _stream(dev)), "fp8rl_expert_rows")
+    return ExpertRows(pos, src, start, count, align)
 
 
 def _layout(rows: ExpertRows, dev) -> "_abi.ExpertLayout":

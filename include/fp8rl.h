@@ -586,8 +586,8 @@ typedef struct {
  * argument is out of its range. */
 FP8RL_API int64_t fp8rl_expert_rows_capacity(int64_t T, int64_t k, int64_t E, int64_t align);
 
-/* Sorts the pairs by expert: index [T][k] -> pos, src, start, count (all written; start and src
- * 16-byte aligned).  An index outside [0, E) is a pair of no expert; the same expert twice in a row
+/* Sorts the pairs by expert: index [T][k] -> pos, src, start, count (all written; 4-byte aligned, as
+ * in every call that takes them).  An index outside [0, E) is a pair of no expert; the same expert twice in a row
  * is two pairs.  1 <= k <= 32, E <= 1024, T k <= 2^30, align 1 or 128.  The workspace, of
  * fp8rl_expert_rows_workspace_bytes (0 for small calls), is written before it is read. */
 FP8RL_API fp8rl_status fp8rl_expert_rows(const int32_t* index, int64_t T, int64_t k, int64_t E, int64_t align,

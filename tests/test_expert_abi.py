@@ -79,8 +79,8 @@ def test_sort_workspace(abi):
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), "INVALID_ARG"), (dict(k=0), "INVALID_ARG"), (dict(E=0), "INVALID_ARG"), (dict(k=33), "SHAPE"), (dict(E=1025), "SHAPE"),
     (dict(align=64), "SHAPE"), (dict(T=1 << 29), "SHAPE"), (dict(index=None), "INVALID_ARG"), (dict(pos=None), "INVALID_ARG"),
-    (dict(src=None), "INVALID_ARG"), (dict(start=None), "INVALID_ARG"), (dict(count=None), "INVALID_ARG"), (dict(src=ODD), "ALIGN"),
-    (dict(start=ODD), "ALIGN"), (dict(index=FAKE + 2), "ALIGN"), (dict(T=4096), "WORKSPACE"),
+    (dict(src=None), "INVALID_ARG"), (dict(start=None), "INVALID_ARG"), (dict(count=None), "INVALID_ARG"), (dict(src=FAKE + 2), "ALIGN"),
+    (dict(start=FAKE + 1), "ALIGN"), (dict(index=FAKE + 2), "ALIGN"), (dict(T=4096), "WORKSPACE"),
     (dict(T=4096, ws=FAKE, ws_bytes=100), "WORKSPACE"), (dict(T=4096, ws=FAKE + 1, ws_bytes=1 << 20), "ALIGN"),
 ])
 def test_expert_rows_refusals(abi, kw, want):
@@ -114,7 +114,7 @@ def test_layout_refusals(abi, kw, want):
     (dict(K=0), {}, "INVALID_ARG"), (dict(ldx=64), {}, "INVALID_ARG"), (dict(K=200, ldx=200), {}, "SHAPE"), (dict(x=None), {}, "INVALID_ARG"),
     (dict(q=None), {}, "INVALID_ARG"), (dict(s=None), {}, "INVALID_ARG"), (dict(qT=FAKE), {}, "INVALID_ARG"), (dict(sT=FAKE), {}, "INVALID_ARG"),
     (dict(qT=FAKE, sT=FAKE), dict(align=1), "SHAPE"), (dict(x=ODD), {}, "ALIGN"), (dict(ldx=132), {}, "ALIGN"), (dict(weight=FAKE + 2), {}, "ALIGN"),
-    (dict(qT=ODD, sT=FAKE), {}, "ALIGN"), ({}, dict(src=None), "INVALID_ARG"), ({}, dict(src=ODD), "ALIGN"), (dict(x=None), dict(T=0), "OK"),
+    (dict(qT=ODD, sT=FAKE), {}, "ALIGN"), ({}, dict(src=None), "INVALID_ARG"), ({}, dict(src=FAKE + 2), "ALIGN"), ({}, dict(pos=None), "INVALID_ARG"), (dict(x=None), dict(T=0), "OK"),
 ])
 def test_gather_refusals(abi, kw, lay, want):
     a = {**dict(x=FAKE, ldx=128, K=128, weight=None, q=FAKE, s=FAKE, qT=None, sT=None), **kw}
