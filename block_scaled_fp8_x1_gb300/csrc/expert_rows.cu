@@ -30,6 +30,7 @@ __device__ __forceinline__ uint4 ldg_v4(const void* p) {
 __global__ void __launch_bounds__(32 * kSortWarps) k_expert_hist(const int32_t* __restrict__ index, int64_t P, int E,
                                                                  int64_t chunk, int32_t* __restrict__ hist) {
     extern __shared__ int32_t s_hist[];
+    grid_dependency_begin();
     for (int e = threadIdx.x; e < E; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min(lo + chunk, P);
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_place(const int32_t*
                                                                   int32_t* __restrict__ src, int32_t* __restrict__ start,
                                                                   int32_t* __restrict__ count) {
     extern __shared__ int32_t s_n[];
+    grid_dependency_begin();
     int32_t* const s_start = s_n + kSortWarps * E;
     int32_t* const s_count = s_start + E + 1;
     __shared__ int32_t s_warp[kSortWarps];
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(256) k_expert_combine(const uint16_t* __restri
                                                         const float* __restrict__ weight, const uint16_t* __restrict__ residual,
                                                         int64_t ldr, const int32_t* __restrict__ pos, int64_t T, int k, int64_t R,
                                                         uint16_t* __restrict__ out, int64_t ldo) {
+    grid_dependency_begin();
     const int64_t per = N / 8;
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < T * per; i += step) {
@@ -190,6 +193,7 @@ __global__ void __launch_bounds__(256) k_expert_dweight(const uint16_t* __restri
                                                         const uint16_t* __restrict__ y, int64_t ldy, int64_t N,
                                                         const int32_t* __restrict__ pos, int64_t P, int k, int64_t R,
                                                         float* __restrict__ dweight) {
+    grid_dependency_begin();
     const int lane = threadIdx.x & 31;
     const int64_t p = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (p >= P) return;
@@ -225,31 +229,32 @@ cudaError_t launch_expert_rows(const int32_t* index, int64_t P, int E, int align
     const int nb = expert_rows_blocks(P);
     const int64_t chunk = (P + nb - 1) / nb;
     if (nb > 1) {
-        k_expert_hist<<<nb, 32 * kSortWarps, (size_t)E * 4, st>>>(index, P, E, chunk, hist);
-        cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dependent(k_expert_hist, dim3(nb), dim3(32 * kSortWarps), (size_t)E * 4, st, index, P, E, chunk, hist);
         if (e != cudaSuccess) return e;
     }
     const size_t smem = ((size_t)kSortWarps * E + 2 * E + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(((size_t)kSortWarps + 2) * kMaxExperts * 4 + 4));
-    if (e != cudaSuccess) return e;
-    k_expert_place<<<nb, 32 * kSortWarps, smem, st>>>(index, P, E, chunk, align, R, hist, pos, src, start, count);
-    return cudaGetLastError();
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)(((size_t)kSortWarps + 2) * kMaxExperts * 4 + 4));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(k_expert_place, dim3(nb), dim3(32 * kSortWarps), smem, st, index, P, E, chunk, align, R, hist, pos, src,
+                            start, count);
 }
 
 cudaError_t launch_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,
                                   int64_t ldr, const fp8rl_expert_layout& l, uint16_t* out, int64_t ldo, cudaStream_t st) {
     const int64_t n = l.T * (N / 8);
     const int64_t blocks = std::min<int64_t>((n + 255) / 256, 1 << 20);
-    k_expert_combine<<<(unsigned)blocks, 256, 0, st>>>(y, ldy, N, weight, residual, ldr, l.pos, l.T, (int)l.k, l.R, out, ldo);
-    return cudaGetLastError();
+    return launch_dependent(k_expert_combine, dim3((unsigned)blocks), dim3(256), 0, st, y, ldy, N, weight, residual, ldr, l.pos, l.T,
+                            (int)l.k, l.R, out, ldo);
 }
 
 cudaError_t launch_expert_dweight(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t ldy, int64_t N,
                                   const fp8rl_expert_layout& l, float* dweight, cudaStream_t st) {
     const int64_t P = l.T * l.k;
-    k_expert_dweight<<<(unsigned)((P + 7) / 8), 256, 0, st>>>(dout, ldd, y, ldy, N, l.pos, P, (int)l.k, l.R, dweight);
-    return cudaGetLastError();
+    return launch_dependent(k_expert_dweight, dim3((unsigned)((P + 7) / 8)), dim3(256), 0, st, dout, ldd, y, ldy, N, l.pos, P,
+                            (int)l.k, l.R, dweight);
 }
 
 }  // namespace fp8rl

@@ -198,6 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
         tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish_pair();
     }
+    grid_dependency_begin();
     if (warp == 2) {
         // the starts, and the experts' tiles by a running sum over 32 experts at a time
         int32_t carry = 0;
@@ -528,8 +529,8 @@ cudaError_t launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtenso
     if (most > 227 * 1024) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
-    kern<<<2 * clusters, x_threads(XSmem<WGRAD>::EPI), XSmem<WGRAD>::bytes(p.E), st>>>(ta, tb, tsa, tsb, tc, p);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(2 * clusters), dim3(x_threads(XSmem<WGRAD>::EPI)), XSmem<WGRAD>::bytes(p.E), st, ta, tb, tsa,
+                            tsb, tc, p);
 }
 
 }  // namespace

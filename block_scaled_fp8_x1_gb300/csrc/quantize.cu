@@ -1003,6 +1003,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
 // ------------------------------------------------------------------------------------
 template <bool WEIGHTED>
 __global__ void __launch_bounds__(128) k_scatter_rows(const PanelArgs a, const int32_t* __restrict__ pos) {
+    grid_dependency_begin();
     const int lane = threadIdx.x & 31, half = lane >> 4, cl = lane & 15;
     const int R0 = 8 * half, C0 = 8 * cl;
     const int ntiles = (int)(a.K / 128);
@@ -1425,9 +1426,7 @@ cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, cons
     if (qT) return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
     const int64_t items = (l.T + 15) / 16 * (K / 128);
     const int64_t blocks = std::min<int64_t>((items + 3) / 4, (int64_t)num_sms * 8);
-    if (weight) k_scatter_rows<true><<<(unsigned)blocks, 128, 0, st>>>(a, l.pos);
-    else k_scatter_rows<false><<<(unsigned)blocks, 128, 0, st>>>(a, l.pos);
-    return cudaGetLastError();
+    return launch_dependent(weight ? k_scatter_rows<true> : k_scatter_rows<false>, dim3((unsigned)blocks), dim3(128), 0, st, a, l.pos);
 }
 
 cudaError_t launch_silu_mul_quant(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s,
