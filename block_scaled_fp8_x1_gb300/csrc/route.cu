@@ -59,7 +59,7 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 
 // The NL neighbours from e0 on of a row at p + base, -inf (or `none`) behind the last of E; in pieces of
 // up to 16 bytes where `vec` says that rows are aligned to them (one number at a time touches every
-// 32-byte sector of the row once for each of the NL: 26 us instead of AFTER_US).
+// 32-byte sector of the row up to 8 times).
 template <int NL, bool BF16>
 __device__ __forceinline__ void load_lane(const void* p, int64_t base, int e0, int E, bool vec, float none, float (&z)[NL]) {
     constexpr int BYTES = NL * (BF16 ? 2 : 4);
