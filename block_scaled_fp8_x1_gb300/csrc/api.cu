@@ -1372,7 +1372,7 @@ fp8rl_status fp8rl_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, con
     fp8rl_status e = check_layout(rows, "p");
     if (e != FP8RL_OK) return e;
     if (N <= 0 || ldy < N || ldo < N || (residual && ldr < N)) return FP8RL_ERR_INVALID_ARG;
-    if (N % 8 != 0) return FP8RL_ERR_SHAPE;
+    if (N % 8 != 0 || N > kMaxCombineColumns) return FP8RL_ERR_SHAPE;
     if (rows->T == 0) return FP8RL_OK;
     if (!y || !out) return FP8RL_ERR_INVALID_ARG;
     if (!aligned16(y) || !aligned16(out) || !aligned16(residual) || (ldy * 2) % 16 != 0 || (ldo * 2) % 16 != 0 ||

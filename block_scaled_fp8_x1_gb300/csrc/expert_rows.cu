@@ -144,48 +144,56 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_place(const int32_t*
 // ---------------------------------------------------------------- combine
 
 // out[t] = residual[t] + sum_j weight[t, j] y[pos[t, j]] in FP32 in the order of j: a thread has 8
-// columns of one token.  Pairs without a row (pos outside [0, R)) add nothing.
-__global__ void __launch_bounds__(256) k_expert_combine(const uint16_t* __restrict__ y, int64_t ldy, int64_t N,
-                                                        const float* __restrict__ weight, const uint16_t* __restrict__ residual,
-                                                        int64_t ldr, const int32_t* __restrict__ pos, int64_t T, int k, int64_t R,
-                                                        uint16_t* __restrict__ out, int64_t ldo) {
+// columns of one token and the rows of up to SLOTS pairs (2, 4 or 8, by k) on their way at once.  Pairs without a row (pos
+// outside [0, R)) add nothing.  A block has kCombine columns / 8 of one token (blockIdx.y: which), or
+// with fewer columns several tokens.
+constexpr int kCombine = 128;
+template <int SLOTS>
+__global__ void __launch_bounds__(kCombine) k_expert_combine(const uint16_t* __restrict__ y, int64_t ldy, int per,
+                                                             const float* __restrict__ weight, const uint16_t* residual,
+                                                             int64_t ldr, const int32_t* __restrict__ pos, int64_t T, int k,
+                                                             int64_t R, uint16_t* out, int64_t ldo) {
     grid_dependency_begin();
-    const int64_t per = N / 8;
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < T * per; i += step) {
-        const int64_t t = i / per, c = (i - t * per) * 8;
-        float acc[8];
+    const int tokens = per < kCombine ? kCombine / per : 1;          // of a block
+    const int mine = tokens > 1 ? (int)threadIdx.x / per : 0;
+    const int chunk = tokens > 1 ? (int)threadIdx.x - mine * per : (int)(blockIdx.y * kCombine + threadIdx.x);
+    const int64_t t = (int64_t)blockIdx.x * tokens + mine;
+    if (mine >= tokens || t >= T || chunk >= per) return;
+    const int64_t c = (int64_t)chunk * 8;
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (residual) res = *reinterpret_cast<const uint4*>(residual + t * ldr + c);
+    float2 acc[4];
+    #pragma unroll
+    for (int h = 0; h < 4; ++h) acc[h] = make_float2(0.0f, 0.0f);
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
+        int row[SLOTS];
+        float w[SLOTS];
         #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-        #pragma unroll 4
-        for (int j = 0; j < k; ++j) {
-            const int r = __ldg(pos + t * k + j);
-            if ((unsigned)r >= (unsigned)R) continue;
-            const float w = weight ? __ldg(weight + t * k + j) : 1.0f;
-            const uint4 v = ldg_v4(y + (int64_t)r * ldy + c);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                acc[2 * h] = fmaf(w, bf16_lo(u[h]), acc[2 * h]);
-                acc[2 * h + 1] = fmaf(w, bf16_hi(u[h]), acc[2 * h + 1]);
-            }
+        for (int j = 0; j < SLOTS; ++j) {
+            row[j] = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+            w[j] = weight && j0 + j < k ? __ldg(weight + t * k + j0 + j) : 1.0f;
         }
-        if (residual) {
-            const uint4 v = ldg_v4(residual + t * ldr + c);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                acc[2 * h] += bf16_lo(u[h]);
-                acc[2 * h + 1] += bf16_hi(u[h]);
-            }
+        uint4 v[SLOTS];
+        #pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const bool has = (unsigned)row[j] < (unsigned)R;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (has) v[j] = ldg_v4(y + (int64_t)row[j] * ldy + c);
+            else w[j] = 0.0f;
         }
-        uint4 o;
-        o.x = pack_bf16x2(acc[0], acc[1]);
-        o.y = pack_bf16x2(acc[2], acc[3]);
-        o.z = pack_bf16x2(acc[4], acc[5]);
-        o.w = pack_bf16x2(acc[6], acc[7]);
-        *reinterpret_cast<uint4*>(out + t * ldo + c) = o;
+        #pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            #pragma unroll
+            for (int h = 0; h < 4; ++h)
+                acc[h] = __ffma2_rn(make_float2(w[j], w[j]), make_float2(bf16_lo(u[h]), bf16_hi(u[h])), acc[h]);
+        }
     }
+    const uint32_t u[4] = {res.x, res.y, res.z, res.w};
+    uint32_t o[4];
+    #pragma unroll
+    for (int h = 0; h < 4; ++h) o[h] = pack_bf16x2(acc[h].x + bf16_lo(u[h]), acc[h].y + bf16_hi(u[h]));
+    *reinterpret_cast<uint4*>(out + t * ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // dweight[t, j] = <dout[t], y[pos[t, j]]>, a warp a pair; 0 for a pair without a row.
@@ -244,10 +252,12 @@ cudaError_t launch_expert_rows(const int32_t* index, int64_t P, int E, int align
 
 cudaError_t launch_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,
                                   int64_t ldr, const fp8rl_expert_layout& l, uint16_t* out, int64_t ldo, cudaStream_t st) {
-    const int64_t n = l.T * (N / 8);
-    const int64_t blocks = std::min<int64_t>((n + 255) / 256, 1 << 20);
-    return launch_dependent(k_expert_combine, dim3((unsigned)blocks), dim3(256), 0, st, y, ldy, N, weight, residual, ldr, l.pos, l.T,
-                            (int)l.k, l.R, out, ldo);
+    const int per = (int)(N / 8);
+    const int tokens = per < kCombine ? kCombine / per : 1;
+    const dim3 grid((unsigned)((l.T + tokens - 1) / tokens), (unsigned)(tokens > 1 ? 1 : (per + kCombine - 1) / kCombine));
+    const auto kern = l.k <= 2 ? k_expert_combine<2> : l.k <= 4 ? k_expert_combine<4> : k_expert_combine<8>;
+    return launch_dependent(kern, grid, dim3(kCombine), 0, st, y, ldy, per, weight, residual, ldr, l.pos, l.T, (int)l.k, l.R, out,
+                            ldo);
 }
 
 cudaError_t launch_expert_dweight(const uint16_t* dout, int64_t ldd, const uint16_t* y, int64_t ldy, int64_t N,

@@ -11,6 +11,7 @@ constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopK = 32;
 constexpr int64_t kMaxGroups = 32;
 constexpr int64_t kMaxPairs = int64_t(1) << 30;
+constexpr int64_t kMaxCombineColumns = int64_t(1) << 24;
 constexpr int64_t kExpertAlign = 128;   // the row alignment that the training forms need
 
 // route.cu

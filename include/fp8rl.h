@@ -607,7 +607,8 @@ FP8RL_API fp8rl_status fp8rl_expert_gather_quant(const uint16_t* x, int64_t ldx,
 /* out[t] = residual[t] + sum_j weight[t][j] y[pos[t][j]], summed in FP32 in the order of j; weight
  * NULL: 1; residual NULL: 0; pairs without a row add nothing.  With weight NULL it is the backward
  * of the gather.
- *   y : BF16 [R][ldy], residual [T][ldr], out [T][ldo], N columns, N % 8 == 0.  out may be residual. */
+ *   y : BF16 [R][ldy], residual [T][ldr], out [T][ldo], N columns, N % 8 == 0,
+ *   at most 2^24.  out may be residual. */
 FP8RL_API fp8rl_status fp8rl_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight,
                                             const uint16_t* residual, int64_t ldr, const fp8rl_expert_layout* rows,
                                             uint16_t* out, int64_t ldo, fp8rl_stream_t stream);
