@@ -696,6 +696,10 @@ class ExpertRows(NamedTuple):
     align: int                             # 128 (training, prefill) or 1 (rollout)
 
 
+class _SortedRows(ExpertRows):
+    """expert_rows' own result: with what the C calls take, which it has checked already."""
+
+
 _SCORES = {"softmax": _abi.FP8RL_SCORE_SOFTMAX, "sigmoid": _abi.FP8RL_SCORE_SIGMOID}
 
 
@@ -782,13 +786,18 @@ def expert_rows(index: torch.Tensor, n_experts: int, align: int = 128) -> Expert
     # a buffer of this call's own: calls may run on several streams
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     at = buf.data_ptr()
-    check(L.fp8rl_expert_rows(index.data_ptr(), T, k, E, align, at + 4 * (R + 2 * n + 1), at, at + 4 * R,
-                              at + 4 * (R + n + 1), _ptr(ws), need, _stream(dev)), "fp8rl_expert_rows")
-    return ExpertRows(pos, src, start, count, align)
+    l = _abi.ExpertLayout(at + 4 * (R + 2 * n + 1), at, at + 4 * R, at + 4 * (R + n + 1), T, k, E, R, align)
+    check(L.fp8rl_expert_rows(index.data_ptr(), T, k, E, align, l.pos, l.src, l.start, l.count, _ptr(ws), need,
+                              _stream(dev)), "fp8rl_expert_rows")
+    rows = _SortedRows(pos, src, start, count, align)
+    rows.layout = l, dev
+    return rows
 
 
 def _layout(rows: ExpertRows, dev) -> "_abi.ExpertLayout":
     """Checks the arrays of an expert order on `dev` and packs them for the C calls."""
+    if type(rows) is _SortedRows and rows.layout[1] == dev:
+        return rows.layout[0]
     pos, src, start, count, align = rows
     _matrix(pos, "rows.pos")
     (T, k), R, E = pos.shape, src.numel(), count.numel()
