@@ -1001,8 +1001,9 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
 // scales of a row go to places of their own, 4 bytes each, which L2 puts together.
 // Rows of the result without a pair are zeroed by the warps as they finish.
 // ------------------------------------------------------------------------------------
+constexpr int scatter_blocks(bool weighted) { return weighted ? 4 : 8; }      // of an SM
 template <bool WEIGHTED>
-__global__ void __launch_bounds__(128) k_scatter_rows(const PanelArgs a, const int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(const PanelArgs a, const int32_t* __restrict__ pos) {
     grid_dependency_begin();
     const int lane = threadIdx.x & 31, half = lane >> 4, cl = lane & 15;
     const int R0 = 8 * half, C0 = 8 * cl;
@@ -1071,11 +1072,12 @@ __global__ void __launch_bounds__(128) k_scatter_rows(const PanelArgs a, const i
             ++rb;
         }
     }
-    // rows of no pair
-    for (int64_t r0 = first * 32; r0 < a.M; r0 += step * 32) {
-        const int p = r0 + lane < a.M ? __ldg(a.src + r0 + lane) : 0;
+    // rows of no pair: they come in runs, so neighbouring rows go to different warps
+    for (int64_t r0 = first; r0 < a.M; r0 += step * 32) {
+        const int64_t mine = r0 + lane * step;
+        const int p = mine < a.M ? __ldg(a.src + mine) : 0;
         for (uint32_t none = __ballot_sync(0xffffffffu, p < 0 || p >= a.x_rows * a.k); none; none &= none - 1) {
-            const int64_t r = r0 + __ffs(none) - 1;
+            const int64_t r = r0 + (__ffs(none) - 1) * step;
             for (int64_t c = lane * 16; c < a.K; c += 512) *reinterpret_cast<uint4*>(a.q + r * a.K + c) = make_uint4(0, 0, 0, 0);
             for (int c = lane; c < ntiles; c += 32) a.s[(int64_t)c * a.M + r] = 0.0f;
         }
@@ -1425,7 +1427,7 @@ cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, cons
     a.timeout_ns = timeout_ns;
     if (qT) return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
     const int64_t items = (l.T + 15) / 16 * (K / 128);
-    const int64_t blocks = std::min<int64_t>((items + 3) / 4, (int64_t)num_sms * 8);
+    const int64_t blocks = std::min<int64_t>((items + 3) / 4, (int64_t)num_sms * scatter_blocks(weight != nullptr));
     return launch_dependent(weight ? k_scatter_rows<true> : k_scatter_rows<false>, dim3((unsigned)blocks), dim3(128), 0, st, a, l.pos);
 }
 
