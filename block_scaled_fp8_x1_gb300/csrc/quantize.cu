@@ -1425,10 +1425,15 @@ cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, cons
     a.x = x; a.ldx = ldx; a.M = l.R; a.K = K; a.q = q; a.s = s; a.qT = qT; a.sT = sT;
     a.src = l.src; a.weight = weight; a.x_rows = l.T; a.k = (int)l.k;
     a.timeout_ns = timeout_ns;
-    if (qT) return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
+    // Both layouts.  With weights every copy of a row is encoded by itself: one pass in expert order for
+    // rows and columns (65536 pairs x 4096: 315 us, against 363 in two).  Without, the rows token by
+    // token and the columns in expert order (280 us, against 291 in one).
+    if (qT && weight) return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
     const int64_t items = (l.T + 15) / 16 * (K / 128);
     const int64_t blocks = std::min<int64_t>((items + 3) / 4, (int64_t)num_sms * scatter_blocks(weight != nullptr));
-    return launch_dependent(weight ? k_scatter_rows<true> : k_scatter_rows<false>, dim3((unsigned)blocks), dim3(128), 0, st, a, l.pos);
+    const cudaError_t e = launch_dependent(weight ? k_scatter_rows<true> : k_scatter_rows<false>, dim3((unsigned)blocks), dim3(128), 0,
+                                           st, a, l.pos);
+    return e != cudaSuccess || !qT ? e : launch_panel_t<PRO_GATHER, false, true>(a, K, 0, st);
 }
 
 cudaError_t launch_silu_mul_quant(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s,
