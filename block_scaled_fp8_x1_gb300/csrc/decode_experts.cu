@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_warp = reinterpret_cast<int*>(tmem_slot + 4);                       // [12] units of a warp's experts
+    int* s_first = s_warp + 12;                                                // expert, first row and rows of this CTA's first unit
     int* s_units = s_warp + 16;                                                // [E + 1] units of the experts before
     int* s_start = s_units + p.E + 1;                                          // [E]
 
@@ -113,12 +114,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_relinquish();
     }
     grid_dependency_begin();
-    // units of the experts before each expert
+    // units of the experts before each expert; the expert of the first unit is found on the way
+    const int first = (int)cluster_idx(), step = (int)cluster_count();
+    const int first_unit = (int)((uint32_t)first / (uint32_t)p.tiles);
     int carry = 0;
     for (int e0 = 0; e0 < p.E; e0 += kThreads) {
         const int e = e0 + (int)threadIdx.x;
-        const int n = e < p.E ? (max(0, __ldg(p.count + e)) + MP - 1) / MP : 0;
-        if (e < p.E) s_start[e] = __ldg(p.start + e);
+        const int rows = e < p.E ? max(0, __ldg(p.count + e)) : 0, start = e < p.E ? __ldg(p.start + e) : 0;
+        const int n = (rows + MP - 1) / MP;
         int scan = n;
         #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -133,9 +136,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (i < warp) scan += s_warp[i];
             total += s_warp[i];
         }
-        if (e < p.E) s_units[e] = carry + scan - n;
+        if (e < p.E) {
+            s_units[e] = carry + scan - n;
+            s_start[e] = start;
+            const int i = first_unit - (carry + scan - n);
+            if (i >= 0 && i < n) {
+                s_first[0] = e;
+                s_first[1] = start + i * MP;
+                s_first[2] = min(MP, rows - i * MP);
+            }
+        }
         carry += total;
-        __syncthreads();
+        if (e0 + kThreads < p.E) __syncthreads();      // s_warp is written again
     }
     if (threadIdx.x == 0) s_units[p.E] = carry;
     tc_fence_before();
@@ -144,7 +156,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tmem_base = *tmem_slot;
     // items of this CTA: first, first + step, ... (one at most where the reduction is split)
     const int items = carry * p.tiles;
-    const int first = (int)cluster_idx(), step = (int)cluster_count();
     bool ok = true;
     // Item -> expert, weight tile and rows
     struct Item {
@@ -154,16 +165,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         Item t;
         const int unit = (int)((uint32_t)item / (uint32_t)p.tiles);
         t.tile = item - unit * p.tiles;
-        int e = 0, above = p.E;          // s_units[e] <= unit < s_units[above]
-        while (above - e > 1) {
-            const int mid = (e + above) >> 1;
-            if (s_units[mid] <= unit) e = mid;
-            else above = mid;
+        if (item == first) {
+            t.expert = s_first[0];
+            t.row0 = s_first[1];
+            t.rows = s_first[2];
+        } else {
+            int e = 0, above = p.E;          // s_units[e] <= unit < s_units[above]
+            while (above - e > 1) {
+                const int mid = (e + above) >> 1;
+                if (s_units[mid] <= unit) e = mid;
+                else above = mid;
+            }
+            t.expert = e;
+            const int before = (unit - s_units[e]) * MP;
+            t.row0 = s_start[e] + before;
+            t.rows = min(MP, max(0, __ldg(p.count + e)) - before);
         }
-        t.expert = e;
-        const int before = (unit - s_units[e]) * MP;
-        t.row0 = s_start[e] + before;
-        t.rows = min(MP, max(0, __ldg(p.count + e)) - before);
         // starts and counts that do not fit the rows: nothing is read or written there
         if (t.row0 < 0 || (int64_t)t.row0 + t.rows > p.R) {
             record_status(FP8RL_ERR_DEVICE_BOUNDS);
