@@ -697,7 +697,12 @@ class ExpertRows(NamedTuple):
 
 
 class _SortedRows(ExpertRows):
-    """expert_rows' own result: with what the C calls take, which it has checked already."""
+    """expert_rows' own result: with what the C calls take, which it has checked already (a copy is
+    a plain ExpertRows)."""
+    layout = None
+
+    def __reduce__(self):
+        return ExpertRows, tuple(self)
 
 
 _SCORES = {"softmax": _abi.FP8RL_SCORE_SOFTMAX, "sigmoid": _abi.FP8RL_SCORE_SIGMOID}
@@ -796,8 +801,10 @@ def expert_rows(index: torch.Tensor, n_experts: int, align: int = 128) -> Expert
 
 def _layout(rows: ExpertRows, dev) -> "_abi.ExpertLayout":
     """Checks the arrays of an expert order on `dev` and packs them for the C calls."""
-    if type(rows) is _SortedRows and rows.layout[1] == dev:
-        return rows.layout[0]
+    if type(rows) is _SortedRows and rows.layout is not None:
+        l, on = rows.layout
+        if on == dev and (l.pos, l.src, l.start, l.count) == tuple(t.data_ptr() for t in rows[:4]):
+            return l
     pos, src, start, count, align = rows
     _matrix(pos, "rows.pos")
     (T, k), R, E = pos.shape, src.numel(), count.numel()

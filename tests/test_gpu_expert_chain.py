@@ -205,3 +205,42 @@ def test_index_of_another_width_or_values_is_safe(fp8lib):
     assert (ys[0].double() - ys[1].double()).abs().max() < 2.0 ** -6 * ys[0].abs().max() + 1e-3 * rms
     none = torch.tensor(((idx < 0) | (idx >= E)).all(1), device=DEV)
     assert (ys[0][none] == 0).all()
+
+
+def test_order_captured_with_its_workspace(fp8lib):
+    """A large order (two kernels and a workspace) captured twice in one graph and replayed."""
+    T, E, k = 3000, 60, 4
+    idx = [torch.randint(0, E, (T, k), dtype=torch.int32, device=DEV) for _ in range(2)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        fp8lib.expert_rows(idx[0], E)
+        with torch.cuda.graph(g, stream=s):
+            rows = [fp8lib.expert_rows(i, E, a) for i, a in zip(idx, (1, 128))]
+    for seed in range(2):
+        for i in idx:
+            i.copy_(torch.randint(-1, E, (T, k), dtype=torch.int32, device=DEV))
+        g.replay()
+        torch.cuda.synchronize()
+        for i, r in zip(idx, rows):
+            want = fp8lib.expert_rows(i, E, r.align)
+            assert all(torch.equal(a, b) for a, b in zip(r[:4], want[:4]))
+
+
+def test_copies_of_an_order(fp8lib):
+    """An order that was copied, moved or built from tensors gives what the original gives."""
+    import copy
+    idx = torch.randint(0, 8, (40, 2), dtype=torch.int32, device=DEV)
+    rows = fp8lib.expert_rows(idx, 8)
+    x = torch.randn((40, 256), device=DEV).to(torch.bfloat16)
+    want = fp8lib.expert_gather_quant(x, rows)
+    other = fp8lib.expert_rows(idx.flip(0).contiguous(), 8)
+    for r in (fp8lib.ExpertRows(*rows), copy.deepcopy(rows), copy.copy(rows), rows._replace(src=rows.src.clone()),
+              other._replace(pos=rows.pos, src=rows.src, start=rows.start, count=rows.count)):
+        got = fp8lib.expert_gather_quant(x, r)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError, match="rows.count"):
+        fp8lib.expert_gather_quant(x, rows._replace(count=rows.count.cpu()))
+    with pytest.raises(RuntimeError, match="SHAPE"):
+        fp8lib.expert_gather_quant(x, rows._replace(src=rows.src[:-1]))

@@ -73,6 +73,47 @@ def test_route_near_ties(fp8lib):
             assert np.array_equal(ints(got.index), i), (score, kw)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("spread", [0.5, 2.0])
+def test_route_order_of_scores_that_nearly_agree(fp8lib, spread, score):
+    """Biases that bring every score to within their own rounding (2^-27 and less) of one value: the
+    order is that of the exact sums wherever these are 2^-38 apart."""
+    for seed in range(8):
+        r = np.random.default_rng(seed)
+        z = (spread * r.uniform(-1, 1, (1, 64))).astype(np.float32)
+        s = ref.scores(z.astype(np.float64), score)
+        b = (s.mean() - s[0]).astype(np.float32)
+        i = ints(fp8lib.route_topk(torch.tensor(z, device=DEV), 8, score=score, bias=torch.tensor(b, device=DEV), group_rank=1).index)[0]
+        v = s[0] + b.astype(np.float64)
+        assert len(set(i.tolist())) == 8
+        assert np.all(v[i[:-1]] >= v[i[1:]] - 2.0 ** -38)
+        assert v[i].min() >= np.delete(v, i).max() - 2.0 ** -38
+
+
+def test_route_without_differences(fp8lib):
+    """All logits and biases equal, in every form of the selection: the first experts, in order."""
+    for E, k in ((1, 1), (64, 8), (100, 32), (256, 8), (1024, 3)):
+        for dtype in (torch.float32, torch.bfloat16):
+            z = torch.full((3, E), 0.25, dtype=dtype, device=DEV)
+            for bias in (None, torch.zeros(E, device=DEV)):
+                for score in ("softmax", "sigmoid"):
+                    r = fp8lib.route_topk(z, k, score=score, bias=bias)
+                    assert ints(r.index).tolist() == [list(range(k))] * 3
+                    assert np.abs(np64(r.weight) - 1.0 / k).max() < 1e-6
+
+
+@pytest.mark.parametrize("off", [0, 1, 2, 3, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_rows_of_any_alignment(fp8lib, off, dtype):
+    wide = torch.randn((20, 300), generator=torch.Generator(DEV).manual_seed(off), device=DEV).to(dtype)
+    for E in (64, 96, 256):
+        z = wide[:, off:off + E]
+        for bias in (None, torch.linspace(-0.1, 0.1, E + 1, device=DEV)[1:]):
+            a = fp8lib.route_topk(z, 6, score="sigmoid", bias=bias)
+            b = fp8lib.route_topk(z.contiguous(), 6, score="sigmoid", bias=None if bias is None else bias.clone())
+            assert torch.equal(a.index, b.index) and torch.equal(a.weight, b.weight)
+
+
 def test_route_equal_scores_go_to_the_lowest_index(fp8lib):
     z = torch.zeros((3, 100), device=DEV)
     z[1, ::2] = -0.0
