@@ -16,9 +16,9 @@
 // memory.  A segment with an odd number of 128-row blocks leaves half of its last pair tile unused
 // (computed on the next expert's rows, not stored).
 //
-// Roles and pipeline as in gemm_pair.cu: warp 0 copies the operands, warp 3 the scales, warp 1
-// issues the MMAs, 8 (forward, DGrad) or 16 (WGrad) epilogue warps promote each K-block's partial
-// sums from one of two 256-column TMEM buffers.  B's block scales come by 4-byte copies, so that any
+// Roles and pipeline as in gemm_pair.cu: warp 2 finds the tiles and announces them to the others,
+// warp 0 copies the operands, warp 3 the scales, warp 1 issues the MMAs, 8 (forward, DGrad) or 16
+// (WGrad) epilogue warps promote each K-block's partial sums from one of two 256-column TMEM buffers.  B's block scales come by 4-byte copies, so that any
 // number of K-blocks and columns will do.
 // Every mbarrier wait is bounded (FP8RL_ERR_DEVICE_TIMEOUT).
 #include "common.cuh"
@@ -51,10 +51,11 @@ struct XSmem {
     static constexpr int SLOT = SLOT_A + (WGRAD ? kPN : 0);
     static constexpr int RING_BYTES = NS * SLOT * 4;
     static constexpr int STAGE_C_BYTES = 128 * kPN * 2;      // the whole result tile, 2 KB boxes
-    static constexpr int NBARS = 2 * STAGES + 2 * kBufs + 2 * NS + 1;
+    static constexpr int NT = 4;                          // tiles announced ahead
+    static constexpr int NBARS = 2 * STAGES + 2 * kBufs + 2 * NS + 2 * NT + 1;
     static size_t bytes(int E) {
         return 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + STAGE_C_BYTES + RING_BYTES + NBARS * 8 + 16 +
-               2 * (size_t)(E + 1) * 4;
+               NT * 32 + 2 * (size_t)(E + 1) * 4;
     }
 };
 
@@ -74,29 +75,18 @@ struct XWalk {
     const int32_t* start;     // [E + 1]
     const int32_t* tiles;     // forward, DGrad: [E + 1] tiles of the experts before
     int E, n_tiles, rows, nkb;
-    int e, before;            // current expert, WGrad: tiles of the experts before it
+    int e;                    // current expert
     __device__ __forceinline__ int total() const {
         return WGRAD ? E * ((rows + 255) / 256) * n_tiles : tiles[E];
-    }
-    // WGrad: advances to the expert of `item` and returns its K-blocks (else the constant)
-    __device__ __forceinline__ int blocks(int item) {
-        if (!WGRAD) return nkb;
-        const int per = ((rows + 255) / 256) * n_tiles;
-        while (item - before >= per) {
-            before += per;
-            ++e;
-        }
-        return max(0, start[e + 1] - start[e]) >> 7;
     }
     __device__ __forceinline__ XTile at(int item, int rank) {
         XTile t;
         int m, n, units;
         if (WGRAD) {
-            t.nkb = blocks(item);
-            item -= before;
             units = (rows + 255) / 256;
+            e = item / (units * n_tiles);
+            item -= e * units * n_tiles;
         } else {
-            t.nkb = nkb;
             if (tiles[e + 1] <= item) {      // tiles[e] <= item < tiles[above]
                 int above = E;
                 while (above - e > 1) {
@@ -109,25 +99,20 @@ struct XWalk {
             units = (start[e + 1] - start[e] + 255) / 256;
         }
         // within an expert 16 row units at a time sweep the columns, which keeps their rows (16 MB
-        // at 4096 columns) and the expert's weights in L2.  Up to 16 units that is one division,
-        // which a reciprocal gives exactly (item * units < 2^22): the warps compute it between two
-        // tiles, where an integer division's latency showed.
-        if (units <= 16) {
-            n = (int)(((float)item + 0.5f) * __frcp_rn((float)units));
-            m = item - n * units;
-        } else {
-            raster_tile(item, units, n_tiles, 16, 0, &m, &n);
-        }
+        // at 4096 columns) and the expert's weights in L2
+        raster_tile(item, units, n_tiles, 16, 0, &m, &n);
         t.e = e;
         t.col = n * kPN;
         if (WGRAD) {
             t.row = m * 256 + rank * 128;
             t.row_end = rows;
             t.kb0 = start[e] >> 7;
+            t.nkb = max(0, start[e + 1] - start[e]) >> 7;
         } else {
             t.row = start[e] + m * 256 + rank * 128;
             t.row_end = start[e + 1];
             t.kb0 = 0;
+            t.nkb = nkb;
         }
         return t;
     }
@@ -157,10 +142,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
     uint64_t* tempty_bar = tfull_bar + kBufs;        // [bufs] both epilogues -> MMA (leader's)
     uint64_t* sfull_bar = tempty_bar + kBufs;        // [NS] scale copies -> epilogue
     uint64_t* sempty_bar = sfull_bar + NS;           // [NS] epilogue -> scale copies
-    uint64_t* drain_bar = sempty_bar + NS;           // [1] MMA completion at exit (leader)
+    uint64_t* dfull_bar = sempty_bar + NS;           // [NT] a tile announced -> all roles
+    uint64_t* dempty_bar = dfull_bar + S::NT;        // [NT] all roles have it -> the next
+    uint64_t* drain_bar = dempty_bar + S::NT;        // [1] MMA completion at exit (leader)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int32_t* s_start = reinterpret_cast<int32_t*>(tmem_slot + 4);         // [E + 1]
+    int32_t* s_tile = reinterpret_cast<int32_t*>(tmem_slot + 2);          // [NT][8], 16-byte aligned
+    static_assert(S::NBARS % 2 == 1 && S::RING_BYTES % 16 == 0, "alignment of the announced tiles");
+    int32_t* s_start = s_tile + S::NT * 8;                                // [E + 1]
     int32_t* s_tiles = s_start + p.E + 1;                                 // [E + 1]
 
     const int warp = threadIdx.x >> 5;
@@ -184,6 +173,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&sfull_bar[s]), 1);
             mbar_init(smem_u32(&sempty_bar[s]), EPI);
+        }
+        for (int s = 0; s < S::NT; ++s) {
+            mbar_init(smem_u32(&dfull_bar[s]), 1);
+            mbar_init(smem_u32(&dempty_bar[s]), EPI + 2 + (leader ? 1 : 0));   // epilogue, copies, scales, MMA
         }
         mbar_init(smem_u32(drain_bar), 1);
         *abort_flag = 0;
@@ -225,8 +218,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
     cluster_sync_all();   // both CTAs' barriers initialised, TMEM allocated, starts in place
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    XWalk<WGRAD> walk{s_start, s_tiles, p.E, n_tiles, p.rows, p.nkb, 0, 0};
+    XWalk<WGRAD> walk{s_start, s_tiles, p.E, n_tiles, p.rows, p.nkb, 0};
     const int num_items = walk.total();
+    // This CTA's n-th tile, from the warp that works them out: every role waits for it once, reads it
+    // and gives its place back.
+    auto announced = [&](uint32_t n) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&dfull_bar[n % S::NT]), (n / S::NT) & 1, p.timeout_ns, abort_flag));
+    };
+    auto told = [&](uint32_t n) {
+        const int4* d = reinterpret_cast<const int4*>(s_tile + (n % S::NT) * 8);
+        const int4 a = d[0], b = d[1];
+        return XTile{a.x, a.y, a.z, a.w, b.x, b.y};
+    };
+    auto taken = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dempty_bar[n % S::NT]));
+    };
 
     if (warp < 4) {
         warpgroup_reg_dealloc<x_reg_lo(EPI)>();
@@ -234,10 +241,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             // ------------------------------------------------------------ copies
             const uint64_t pol = l2_policy_evict_last();
             const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);   // the leader's
-            uint32_t it = 0;
+            uint32_t it = 0, nt = 0;
             bool ok = true;
             for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
-                const XTile t = walk.at(item, (int)rank);
+                ok = announced(nt);
+                if (!ok) break;
+                const XTile t = told(nt);
+                taken(nt++);
                 const int ax = WGRAD ? t.kb0 * 128 : 0;                       // first reduction column of A
                 const int bx = WGRAD ? t.kb0 * 128 : t.e * p.b_x;             // and of B
                 const int by = (WGRAD ? 0 : t.e * p.b_y) + t.col + (int)rank * (kPN / 2);
@@ -262,6 +272,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                 for (uint32_t j = it - n_out; j < it; ++j)
                     mbar_wait(smem_u32(&full_bar[j % kStages]), (j / kStages) & 1, p.timeout_ns, &no_abort);
             }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ tiles
+            // worked out here, ahead of the others: the epilogue warps, whose chain bounds a tile, lost
+            // 0.6 us a tile finding it by themselves
+            uint32_t nt = 0;
+            for (int item = (int)cid; item < num_items; item += (int)ncl, ++nt) {
+                const XTile t = walk.at(item, (int)rank);
+                const uint32_t d = nt % S::NT;
+                if (!mbar_wait(smem_u32(&dempty_bar[d]), ((nt / S::NT) & 1) ^ 1, p.timeout_ns, abort_flag)) break;
+                if (lane == 0) {
+                    *reinterpret_cast<int4*>(s_tile + d * 8) = make_int4(t.e, t.row, t.row_end, t.col);
+                    *reinterpret_cast<int4*>(s_tile + d * 8 + 4) = make_int4(t.kb0, t.nkb, 0, 0);
+                    mbar_arrive(smem_u32(&dfull_bar[d]));
+                }
+                __syncwarp();
+            }
         } else if (warp == 3) {
             // ------------------------------------------------------------ scales
             // a warp of their own, so that they run ahead of the operands by the whole scale ring
@@ -269,10 +295,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             // of 5 K-blocks the epilogue waited for them
             const uint64_t pol = l2_policy_evict_last();
             const int sgrp = WGRAD ? 1 : (p.nkb < S::SG ? p.nkb : S::SG);
-            uint32_t it = 0;
+            uint32_t it = 0, nt = 0;
             bool ok = true;
             for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
-                const XTile t = walk.at(item, (int)rank);
+                ok = announced(nt);
+                if (!ok) break;
+                const XTile t = told(nt);
+                taken(nt++);
                 for (int kb = 0; kb < t.nkb; kb += S::SG, ++it) {
                     const uint32_t ss = it % NS;
                     if (!mbar_wait(smem_u32(&sempty_bar[ss]), ((it / NS) & 1) ^ 1, p.timeout_ns, abort_flag)) {
@@ -295,11 +324,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                 mbar_wait(smem_u32(&sfull_bar[j % NS]), (j / NS) & 1, p.timeout_ns, &no_abort);
         } else if (warp == 1 && leader) {
             // ------------------------------------------------------------ MMA issuer
-            uint32_t it = 0;
+            uint32_t it = 0, nt = 0;
             bool ok = true;
             const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
             for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
-                const int nkb = walk.blocks(item);
+                ok = announced(nt);
+                if (!ok) break;
+                const XTile t = told(nt);
+                taken(nt++);
+                const int nkb = t.nkb;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const uint32_t ts = it % kBufs;
                     const uint32_t s = it % kStages;
@@ -343,31 +376,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
         };
         uint32_t acc_it = 0, g_done = 0;
         bool ok = true;
-        XTile t = {};
         float sb_cur = 0.0f, sb_nxt = 0.0f;      // lane l: the scale of K-block l of 32
         if ((int)cid < num_items) {
-            t = walk.at((int)cid, (int)rank);
-            if (!WGRAD) sb_nxt = b_scale(t, lane);
+            ok = announced(0);
+            if (!WGRAD && ok) sb_nxt = b_scale(told(0), lane);
         }
-        for (int item = (int)cid; ok && item < num_items; item += (int)ncl) {
+        uint32_t nt = 0;
+        for (int item = (int)cid; ok && item < num_items; item += (int)ncl, ++nt) {
             const bool more = item + (int)ncl < num_items;
-            const XTile next = more ? walk.at(item + (int)ncl, (int)rank) : t;
+            if (more) ok = announced(nt + 1);
+            if (!ok) break;
+            const int nkb = told(nt).nkb;
             float2 acc[COLS / 2];
             #pragma unroll
             for (int c = 0; c < COLS / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
 
-            for (int kb = 0; kb < t.nkb; ++kb, ++acc_it) {
+            for (int kb = 0; kb < nkb; ++kb, ++acc_it) {
                 if (!WGRAD && (kb & 31) == 0) {
                     sb_cur = sb_nxt;
-                    if (kb + 32 < t.nkb) sb_nxt = b_scale(t, kb + 32 + lane);
-                    else if (more) sb_nxt = b_scale(next, lane);
+                    if (kb + 32 < nkb) sb_nxt = b_scale(told(nt), kb + 32 + lane);
+                    else if (more) sb_nxt = b_scale(told(nt + 1), lane);
                 }
                 const uint32_t gi = WGRAD ? acc_it : g_done;
                 const uint32_t ss = gi % NS;
                 const uint32_t ts = acc_it % kBufs;
                 const int q = kb % S::SG;
                 const bool g_first = q == 0;
-                const bool g_last = kb + 1 == t.nkb || q == S::SG - 1;
+                const bool g_last = kb + 1 == nkb || q == S::SG - 1;
                 bool got = true;
                 if (g_first) got = mbar_wait(smem_u32(&sfull_bar[ss]), (gi / NS) & 1, p.timeout_ns, abort_flag);
                 got = got && mbar_wait(smem_u32(&tfull_bar[ts]), (acc_it / kBufs) & 1, p.timeout_ns, abort_flag);
@@ -463,6 +498,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             // the 16-byte chunk c of row r sits at chunk c ^ ((r >> 1) & 3)), written by TMA,
             // which clips columns outside C; rows behind the segment (or the expert's result)
             // are not stored.
+            const XTile t = told(nt);
+            taken(nt);
             const int y0 = t.row + quad * 32;
             const int yc = (WGRAD ? t.e * p.rows : 0) + y0;
             if (lane == 0) bulk_wait_read<0>();      // the previous tile's stores have read the boxes
@@ -506,7 +543,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                 }
                 bulk_commit();
             }
-            t = next;
         }
         if (lane == 0) bulk_wait_all();   // tile stores complete before exit
     }
