@@ -140,16 +140,16 @@ size_t decode_ws_bytes(int64_t M, int64_t N, int64_t K, int splits) {
 }
 
 // 2-D tensor map of the BF16 output C [rows][ld] (ld a multiple of 8) for the GEMM's tile
-// stores: 32 x 32 boxes, 64-byte swizzle.
-fp8rl_status make_tmap_out(CUtensorMap* m, uint16_t* base, int64_t rows, int64_t cols, int64_t ld) {
+// stores: boxes of 32 rows x 32 columns (64-byte swizzle) or 64 (128-byte).
+fp8rl_status make_tmap_out(CUtensorMap* m, uint16_t* base, int64_t rows, int64_t cols, int64_t ld, int box_cols = 32) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return FP8RL_ERR_CUDA;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {32u, 32u};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, 32u};
     cuuint32_t es[2] = {1u, 1u};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FP8RL_OK : FP8RL_ERR_CUDA;
 }
@@ -1215,11 +1215,11 @@ fp8rl_status run_gemm_experts(ExpertOp op, const ExpertArgs& g, const fp8rl_expe
     if (wgrad) {
         if ((e = make_tmap_scales(&tsa, g.sa, l.R / 128, g.N, 128, 1)) != FP8RL_OK) return e;
         if ((e = make_tmap_scales(&tsb, g.sb, l.R / 128, g.K, 256, 1)) != FP8RL_OK) return e;
-        e = make_tmap_out(&tc, g.c, l.E * g.N, g.K, g.K);
+        e = make_tmap_out(&tc, g.c, l.E * g.N, g.K, g.K, 64);
     } else {
         if ((e = make_tmap_scales(&tsa, g.sa, kr / 128, l.R, 128, (int)std::min<int64_t>(4, kr / 128))) != FP8RL_OK) return e;
         tsb = tsa;   // unused
-        e = make_tmap_out(&tc, g.c, l.R, cols, cols);
+        e = make_tmap_out(&tc, g.c, l.R, cols, cols, 64);
     }
     if (e != FP8RL_OK) return e;
     ExpertGemmParams p = {};

@@ -50,7 +50,7 @@ struct XSmem {
     static constexpr int SLOT_A = 128 * SG;               // floats
     static constexpr int SLOT = SLOT_A + (WGRAD ? kPN : 0);
     static constexpr int RING_BYTES = NS * SLOT * 4;
-    static constexpr int STAGE_C_BYTES = 128 * kPN * 2;      // the whole result tile, 2 KB boxes
+    static constexpr int STAGE_C_BYTES = 128 * kPN * 2;      // the whole result tile, 4 KB boxes
     static constexpr int NT = 4;                          // tiles announced ahead
     static constexpr int NBARS = 2 * STAGES + 2 * kBufs + 2 * NS + 2 * NT + 1;
     static size_t bytes(int E) {
@@ -133,7 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + kStages * S::A_BYTES;
-    uint8_t* stage_c = sB + kStages * S::B_BYTES;                         // [warp][box][2 KB]
+    uint8_t* stage_c = sB + kStages * S::B_BYTES;                         // [warp][box][4 KB]
     float* ring = reinterpret_cast<float*>(stage_c + S::STAGE_C_BYTES);   // [NS][SLOT]
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring) + S::RING_BYTES);
     uint64_t* full_bar = bars;                       // [stages] copies of both CTAs -> MMA (leader's)
@@ -488,9 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             }
             if (!ok) break;
 
-            // ---- the warp's 32 rows x COLS columns go out as 32 x 32 BF16 boxes (64-byte swizzle:
-            // the 16-byte chunk c of row r sits at chunk c ^ ((r >> 1) & 3)), written by TMA,
-            // which clips columns outside C; rows behind the segment (or the expert's result)
+            // ---- the warp's 32 rows x COLS columns go out as BF16 boxes of 32 rows x 64 columns
+            // (128-byte swizzle: the 16-byte chunk c of row r sits at chunk c ^ (r & 7)), written by
+            // TMA, which clips columns outside C; rows behind the segment (or the expert's result)
             // are not stored.
             const XTile t = told(nt);
             taken(nt);
@@ -499,8 +499,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             if (lane == 0) bulk_wait_read<0>();      // the previous tile's stores have read the boxes
             __syncwarp();
             #pragma unroll
-            for (int b = 0; b < COLS / 32; ++b) {
-                const uint32_t buf = smem_u32(stage_c + (ew * (COLS / 32) + b) * 2048);
+            for (int b = 0; b < COLS / 64; ++b) {
+                const uint32_t buf = smem_u32(stage_c + (ew * (COLS / 64) + b) * 4096);
                 if constexpr (WGRAD) {
                     // rows g + 8h, columns 8j + 2tq + {0,1}: one BF16 pair per (row, chunk)
                     const int g8 = lane >> 2, tq = lane & 3;
@@ -508,21 +508,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                     for (int h = 0; h < 4; ++h) {
                         const int rl = g8 + 8 * h;
                         #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float2 v = acc[h * (COLS / 8) + b * 4 + c];
-                            st_shared_b32(buf + rl * 64 + ((c ^ ((rl >> 1) & 3)) << 4) + 4 * tq, pack_bf16x2(v.x, v.y));
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 v = acc[h * (COLS / 8) + b * 8 + c];
+                            st_shared_b32(buf + rl * 128 + ((c ^ (rl & 7)) << 4) + 4 * tq, pack_bf16x2(v.x, v.y));
                         }
                     }
                 } else {
                     #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int cc = b * 32 + c * 8;    // first of these 8 columns
+                    for (int c = 0; c < 8; ++c) {
+                        const int cc = b * 64 + c * 8;    // first of these 8 columns
                         uint4 v;
                         v.x = pack_bf16x2(acc[cc / 2 + 0].x, acc[cc / 2 + 0].y);
                         v.y = pack_bf16x2(acc[cc / 2 + 1].x, acc[cc / 2 + 1].y);
                         v.z = pack_bf16x2(acc[cc / 2 + 2].x, acc[cc / 2 + 2].y);
                         v.w = pack_bf16x2(acc[cc / 2 + 3].x, acc[cc / 2 + 3].y);
-                        st_shared_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), v);
+                        st_shared_v4(buf + lane * 128 + ((c ^ (lane & 7)) << 4), v);
                     }
                 }
             }
@@ -530,10 +530,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             __syncwarp();
             if (lane == 0) {
                 #pragma unroll
-                for (int b = 0; b < COLS / 32; ++b) {
-                    const int x = t.col + col_base + b * 32;
+                for (int b = 0; b < COLS / 64; ++b) {
+                    const int x = t.col + col_base + b * 64;
                     if (y0 < t.row_end && x < p.cols)
-                        tma_store_2d(&tmC, smem_u32(stage_c + (ew * (COLS / 32) + b) * 2048), x, yc);
+                        tma_store_2d(&tmC, smem_u32(stage_c + (ew * (COLS / 64) + b) * 4096), x, yc);
                 }
                 bulk_commit();
             }
@@ -567,7 +567,7 @@ cudaError_t launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtenso
 
 // Launch contract (checked by the caller): A's and B's maps have 128 x 128-byte boxes; tsa is A's
 // row-scale map with boxes of 128 x min(4, K-blocks) (WGrad: 128 x 1), tsb (WGrad) B's with boxes of
-// 256 x 1; tc the BF16 output map (32 x 32 boxes).
+// 256 x 1; tc the BF16 output map (boxes of 64 columns x 32 rows).
 cudaError_t launch_gemm_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa, const CUtensorMap& tsb,
                                 const CUtensorMap& tc, const ExpertGemmParams& p, bool wgrad, int clusters, cudaStream_t st) {
     return wgrad ? launch_t<true>(ta, tb, tsa, tsb, tc, p, clusters, st)
