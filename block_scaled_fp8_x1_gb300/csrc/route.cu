@@ -14,9 +14,9 @@
 // are too close for that, those few scores are formed again in pairs of FP32.
 //
 // One warp per row; lane l holds the NL neighbouring experts from l NL on, whose comparisons run on
-// integers that order as the values do (0: cannot be selected), so a step of the selection is a
-// scan of the lane's own values, a redux and a ballot.  The lowest lane, and in it the lowest place,
-// is the lowest index.
+// integers that order as the values do (0: cannot be selected).  The best keys are ranked by counting
+// (sort_best); where that will not do, k steps of a scan of the lane's own values, a redux and a ballot
+// (take_best).  The lowest lane, and in it the lowest place, is the lowest index.
 #include "common.cuh"
 #include "experts.h"
 
