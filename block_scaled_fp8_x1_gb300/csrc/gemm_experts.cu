@@ -502,15 +502,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             for (int b = 0; b < COLS / 64; ++b) {
                 const uint32_t buf = smem_u32(stage_c + (ew * (COLS / 64) + b) * 4096);
                 if constexpr (WGRAD) {
-                    // rows g + 8h, columns 8j + 2tq + {0,1}: one BF16 pair per (row, chunk)
-                    const int g8 = lane >> 2, tq = lane & 3;
+                    // rows g + 8h, columns 8j + 2tq + {0,1}: an 8 x 8 matrix of the fragment a chunk
+                    const int r8 = lane & 7, m4 = lane >> 3;
                     #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        const int rl = g8 + 8 * h;
                         #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float2 v = acc[h * (COLS / 8) + b * 8 + c];
-                            st_shared_b32(buf + rl * 128 + ((c ^ (rl & 7)) << 4) + 4 * tq, pack_bf16x2(v.x, v.y));
+                        for (int c = 0; c < 8; c += 4) {
+                            uint32_t v[4];
+                            #pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 a = acc[h * (COLS / 8) + b * 8 + c + i];
+                                v[i] = pack_bf16x2(a.x, a.y);
+                            }
+                            st_matrix_x4(buf + (r8 + 8 * h) * 128 + (((c + m4) ^ r8) << 4), v);
                         }
                     }
                 } else {
