@@ -18,8 +18,15 @@
 //
 // Roles and pipeline as in gemm_pair.cu: warp 2 finds the tiles and announces them to the others,
 // warp 0 copies the operands, warp 3 the scales, warp 1 issues the MMAs, 8 (forward, DGrad) or 16
-// (WGrad) epilogue warps promote each K-block's partial sums from one of two 256-column TMEM buffers.  B's block scales come by 4-byte copies, so that any
+// (WGrad) epilogue warps promote each K-block's partial sums from one of two 256-column TMEM buffers.
+// B's block scales (forward, DGrad) are read 32 K-blocks ahead, one a lane, and shuffled, so that any
 // number of K-blocks and columns will do.
+//
+// What bounds it: the epilogue, which TMEM's two buffers keep in step with the MMAs.  Forward, 65536 rows
+// of 64 experts: 0.40 us a K-block (0.35 without the promotion, 0.38 with it and no TMEM loads) and 1.8 us
+// a tile; 580 us at 2816 x 4096, 2600 TFLOP/s.  WGrad: 0.56 us a K-block and 1.2 us for the tile's store,
+// 840 us; without the promotion (a multiply and an FMA an element) 590.  The epilogue's registers are full:
+// whatever adds a few to its K loop spills and costs more than it gives.
 // Every mbarrier wait is bounded (FP8RL_ERR_DEVICE_TIMEOUT).
 #include "common.cuh"
 #include "experts.h"
@@ -274,8 +281,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             }
         } else if (warp == 2) {
             // ------------------------------------------------------------ tiles
-            // worked out here, ahead of the others: the epilogue warps, whose chain bounds a tile, lost
-            // 0.6 us a tile finding it by themselves
+            // worked out here, ahead of the others: finding it by themselves cost the epilogue warps 0.6 us
+            // a tile, and six registers of the K loop
             uint32_t nt = 0;
             for (int item = (int)cid; item < num_items; item += (int)ncl, ++nt) {
                 const XTile t = walk.at(item, (int)rank);
@@ -459,8 +466,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
                         if (pp + 1 < NP) tmem_ld_wait(nxt);
                     }
                 } else {
-                    // 32x32b loads: one row and COLS columns per thread, in two loads (of four of 32 columns:
-                    // 3.5 % slower; 32 columns in flight behind the promotion of the 32 before: 1 %)
+                    // 32x32b loads: one row and COLS columns per thread, in two loads (as four of 32 columns
+                    // 3.5% slower, and 1% with each in flight during the promotion of the one before)
                     const uint32_t tb = tmem_base + t_lane + ts * kPN + col_base;
                     const float f = slot[q * 128 + quad * 32 + lane] * __shfl_sync(0xffffffffu, sb_cur, kb & 31);
                     const float2 f2 = make_float2(f, f);
