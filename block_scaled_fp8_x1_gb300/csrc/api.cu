@@ -1263,6 +1263,7 @@ fp8rl_status run_decode_experts(const ExpertArgs& g, const fp8rl_expert_layout& 
     p.E = (int)l.E;
     p.nkb = (int)nkb;
     p.tiles = (int)tiles;
+    p.max_items = (int)items;
     p.sx = g.sa;
     p.R = l.R;
     p.sw = g.sb;

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int carry = 0;
     for (int e0 = 0; e0 < p.E; e0 += kThreads) {
         const int e = e0 + (int)threadIdx.x;
-        const int rows = e < p.E ? max(0, __ldg(p.count + e)) : 0, start = e < p.E ? __ldg(p.start + e) : 0;
+        const int rows = e < p.E ? (int)min((int64_t)max(0, __ldg(p.count + e)), p.R) : 0, start = e < p.E ? __ldg(p.start + e) : 0;
         const int n = (rows + MP - 1) / MP;
         int scan = n;
         #pragma unroll
@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    // items of this CTA: first, first + step, ... (one at most where the reduction is split)
-    const int items = carry * p.tiles;
+    // items of this CTA: first, first + step, ... (one at most where the reduction is split), and no more
+    // than the rows can have, whatever the counts
+    const int items = (int)min((int64_t)max(carry, 0) * p.tiles, (int64_t)p.max_items);
     bool ok = true;
     // Item -> expert, weight tile and rows
     struct Item {

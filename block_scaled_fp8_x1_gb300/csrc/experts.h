@@ -58,6 +58,7 @@ struct ExpertDecodeParams {
     int E;
     int nkb;                 // K / 128
     int tiles;               // N / 128
+    int max_items;           // (unit, tile) items of any counts that fit the rows
     const float* sx;         // sx[kb * R + r]
     int64_t R;
     const float* sw;         // sw[(e * tiles + tile) * nkb + kb]

@@ -201,12 +201,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
     grid_dependency_begin();
     if (warp == 2) {
         // the starts, and the experts' tiles by a running sum over 32 experts at a time
-        int32_t carry = 0;
+        int32_t carry = 0, last = 0;
         for (int e0 = 0; e0 <= p.E; e0 += 32) {
             const int e = e0 + lane;
-            // within [0, R] and aligned whatever the array holds: a copy has to start on 16 bytes
+            // within [0, R], aligned and ascending whatever the array holds: a copy has to start on 16
+            // bytes, and the tiles have to stay as many as R rows can have
             auto at = [&](int i) { return min(max(__ldg(p.start + min(i, p.E)), 0), p.R) & ~127; };
-            const int32_t a = at(e), b = max(a, at(e + 1));
+            int32_t a = max(last, at(e));
+            #pragma unroll
+            for (int o = 1; o < 32; o <<= 1) a = max(a, __shfl_up_sync(0xffffffffu, a, o));
+            const int32_t b = max(a, at(e + 1));
+            last = __shfl_sync(0xffffffffu, a, 31);
             const int32_t n = e < p.E ? ((b - a + 255) / 256) * n_tiles : 0;
             int32_t scan = n;
             #pragma unroll

@@ -244,3 +244,47 @@ def test_copies_of_an_order(fp8lib):
         fp8lib.expert_gather_quant(x, rows._replace(count=rows.count.cpu()))
     with pytest.raises(RuntimeError, match="SHAPE"):
         fp8lib.expert_gather_quant(x, rows._replace(src=rows.src[:-1]))
+
+
+@pytest.mark.parametrize("E", [5, 70])
+def test_starts_and_counts_that_fit_nothing(fp8lib, E):
+    """Starts and counts that no order has (descending, negative, beyond the rows): the products end, and
+    write their own result alone."""
+    T, k, N, K = 150, 3, 256, 384
+    idx = torch.randint(0, E, (T, k), dtype=torch.int32, device=DEV)
+    x = torch.randn((T, K), device=DEV).to(torch.bfloat16)
+    dy = torch.randn((T, N), device=DEV).to(torch.bfloat16)
+    qw, sw, qwT = fp8lib.quantize_128x128((0.05 * torch.randn((E * N, K), device=DEV)).to(torch.bfloat16))
+    big = 2 ** 31 - 1
+
+    def fenced(*shape):
+        """A result between 64 rows on either side that have to stay."""
+        n = int(np.prod(shape))
+        b = torch.full((n + 128 * shape[-1],), 7.0, dtype=torch.bfloat16, device=DEV)
+        return b, b[64 * shape[-1]:][:n].view(shape)
+
+    for align in (128, 1):
+        rows = fp8lib.expert_rows(idx, E, align)
+        R = rows.src.numel()
+        q, s, qT, sT = fp8lib.expert_gather_quant(x, rows, dual=align > 1)
+        if align > 1:
+            qd, sd, qdT, sdT = fp8lib.expert_gather_quant(dy, rows, dual=True)
+        for pattern in ([0, R], [R, 0], [-5, big], [big, -big], [77, 300]):
+            start = torch.tensor((pattern * E)[:E + 1], dtype=torch.int32, device=DEV)
+            for count in ([R], [big], [-big, big], [1, R + 1]):
+                count = torch.tensor((count * E)[:E], dtype=torch.int32, device=DEV)
+                bad = fp8lib.ExpertRows(rows.pos, rows.src, start, count, align)
+                runs = [(lambda o: fp8lib.gemm_experts_fwd(q, s, qw, sw, bad, out=o), (R, N))]
+                if align > 1:
+                    runs += [(lambda o: fp8lib.gemm_experts_dgrad(qd, sd, qwT, sw, bad, out=o), (R, K)),
+                             (lambda o: fp8lib.gemm_experts_wgrad(qdT, sdT, qT, sT, bad, out=o), (E, N, K))]
+                for f, shape in runs:
+                    b, o = fenced(*shape)
+                    f(o)
+                    status = fp8lib.check_status()
+                    assert status in (0, 8) if align == 1 else status == 0
+                    edge = 64 * shape[-1]
+                    assert (b[:edge] == 7).all() and (b[b.numel() - edge:] == 7).all()
+        last = int(rows.start[-1])
+        y = [fp8lib.gemm_experts_fwd(q, s, qw, sw, r)[:last] for r in (rows, fp8lib.ExpertRows(*rows))]
+        assert torch.equal(*y) and fp8lib.check_status() == 0
