@@ -1364,7 +1364,7 @@ fp8rl_status fp8rl_expert_gather_quant(const uint16_t* x, int64_t ldx, int64_t K
         return FP8RL_ERR_ALIGN;
     int sms = 0;
     if ((e = current_device(&sms)) != FP8RL_OK) return e;
-    return cuda_status(launch_expert_gather(x, ldx, K, weight, *rows, q, s, qT, sT, sms, g_timeout_ns.load(), stream));
+    return cuda_status(launch_expert_gather(x, ldx, K, weight, *rows, q, s, qT, sT, sms, stream));
 }
 
 fp8rl_status fp8rl_expert_combine(const uint16_t* y, int64_t ldy, int64_t N, const float* weight, const uint16_t* residual,

@@ -30,8 +30,7 @@ cudaError_t launch_expert_dweight(const uint16_t* dout, int64_t ldd, const uint1
 
 // quantize.cu: the gathered rows quantized 1x128 and, with qT, 128x1 (l.R % 128 == 0 then).
 cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, const float* weight, const fp8rl_expert_layout& l,
-                                 uint8_t* q, float* s, uint8_t* qT, float* sT, int num_sms, uint64_t timeout_ns,
-                                 cudaStream_t st);
+                                 uint8_t* q, float* s, uint8_t* qT, float* sT, int num_sms, cudaStream_t st);
 
 // gemm_experts.cu: the paired-SM GEMM over the experts' row segments (aligned to 128).
 enum ExpertOp : int { EXPERT_FWD = 0, EXPERT_DGRAD = 1, EXPERT_WGRAD = 2 };

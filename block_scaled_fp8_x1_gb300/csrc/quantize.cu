@@ -96,10 +96,8 @@ __global__ void __launch_bounds__(256) k_quant_1x128(const uint16_t* __restrict_
 // PRO_SILU_BWD from that checkpoint: 989 us at 16384 x 27648 dual (0.56; from BF16 1061 us).  Both
 // use 55 to 58% of the issue slots: three or four encodes and a sigmoid per element, each a chain of
 // dependent instructions, with 16 warps an SM to fill the gaps.
-// PRO_GATHER quantizes rows of x in the order of an index (an expert's rows together), each times a
-// weight where one is given and rounded to BF16; rows without a source are zeros.
 enum Prologue : int { PRO_COPY = 0, PRO_SILU = 1, PRO_RMSNORM = 2, PRO_RMSNORM_G = 3, PRO_SILU_BWD = 5,
-                      PRO_DEQUANT = 6, PRO_SILU_BWD_CK = 7, PRO_SILU_CK = 8, PRO_GATHER = 9 };
+                      PRO_DEQUANT = 6, PRO_SILU_BWD_CK = 7, PRO_SILU_CK = 8 };
 
 struct PanelArgs {
     const uint16_t* x;      // COPY / RMSNORM: x[M][ldx];  SILU: gu[M][ldx], ldx = 2*K;
@@ -119,12 +117,6 @@ struct PanelArgs {
     float* sT;              // scales sT[M/128][K]
     int tiles_per_cta;      // RMSNorm: 128-column sub-tiles handled by one CTA of a panel's cluster
     uint64_t timeout_ns;    // bound of every wait on a TMA copy
-    // GATHER: x[x_rows][ldx]; row m of the result comes from pair p = src[m], row p / k of x, and is
-    // multiplied by weight[p] (nullable); zeros where p is outside [0, k x_rows)
-    const int32_t* src;
-    const float* weight;
-    int64_t x_rows;
-    int k;
 };
 
 // Accurate sum of squares: binary32 pairs (hi, lo) updated with the exact two-sum, so
@@ -339,11 +331,9 @@ __device__ __noinline__ uint4 encode4_slow(float2 x0, float2 x1, float2 x2, floa
                       e4m3x2(__fdiv_rn(x2.x, s), __fdiv_rn(x2.y, s)), e4m3x2(__fdiv_rn(x3.x, s), __fdiv_rn(x3.y, s)));
 }
 
-// 1x128 codes of one thread's 8 rows x 8 columns, a row's group being the 16 lanes of the
-// half-warp: row(i, lo, hi) gets those of row i.  Lane cl returns the scale of row cl & 7, which
-// scale(s) gets before.
-template <typename SCALE, typename ROW>
-__device__ __forceinline__ void encode_rows_8x8(const uint32_t (&w)[8][4], int lane, SCALE&& scale, ROW&& row) {
+// The largest magnitudes (BF16 bits) of one thread's 8 rows x 8 columns, a row's group being the 16
+// lanes of the half-warp: lane cl gets that of row cl & 7.
+__device__ __forceinline__ uint32_t row_maximum_8x8(const uint32_t (&w)[8][4], int lane) {
     const int cl = lane & 15;
     uint32_t pm[4];   // maxima of rows (2k, 2k + 1), a half each
     #pragma unroll
@@ -362,8 +352,14 @@ __device__ __forceinline__ void encode_rows_8x8(const uint32_t (&w)[8][4], int l
         for (int k = 0; k < 4; ++k) pm[k] = __vmaxu2(pm[k], __shfl_xor_sync(0xffffffffu, pm[k], off));
     const int ri = cl & 7;   // this lane forms the scale of row r0 + ri
     const uint32_t pw = (ri >> 1) == 0 ? pm[0] : (ri >> 1) == 1 ? pm[1] : (ri >> 1) == 2 ? pm[2] : pm[3];
-    const uint32_t mine = (ri & 1) ? (pw >> 16) : (pw & 0xFFFFu);
-    const FastScale fs = fast_scale(bf16_bits_amax_to_f32(mine));
+    return (ri & 1) ? (pw >> 16) : (pw & 0xFFFFu);
+}
+
+// 1x128 codes of those rows from their maxima: row(i, lo, hi) gets the codes of row i, before that
+// scale(s) the scale of row cl & 7.
+template <typename SCALE, typename ROW>
+__device__ __forceinline__ void encode_rows_8x8(const uint32_t (&w)[8][4], uint32_t maximum, int lane, SCALE&& scale, ROW&& row) {
+    const FastScale fs = fast_scale(bf16_bits_amax_to_f32(maximum));
     scale(fs.s);
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -390,7 +386,7 @@ __device__ __forceinline__ void encode_rows_8x8(const uint32_t (&w)[8][4], int l
 __device__ __forceinline__ void quant_rows_8x8(const uint32_t (&w)[8][4], uint8_t* q, float* s, int64_t ldq, int64_t M,
                                                int64_t r0, int64_t tt, int C0, int lane) {
     const int cl = lane & 15;
-    encode_rows_8x8(w, lane, [&](float sc) { if (cl < 8 && r0 + cl < M) s[tt * M + r0 + cl] = sc; },
+    encode_rows_8x8(w, row_maximum_8x8(w, lane), lane, [&](float sc) { if (cl < 8 && r0 + cl < M) s[tt * M + r0 + cl] = sc; },
                     [&](int i, uint32_t lo, uint32_t hi) { if (r0 + i < M) stg_v2(q + (r0 + i) * ldq + tt * 128 + C0, lo, hi); });
 }
 
@@ -547,59 +543,10 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         }
     };
     int issued = 0;
-    // GATHER: every thread copies its own 8 rows x 16 bytes of a tile by cp.async and reads them
-    // back itself, so neither copy nor wait needs the other threads.  Lane cl holds what concerns
-    // row R0 + (cl & 7) of its half: the row of x (-1: none, zeros), looked up an item before it is
-    // requested, and the factors of the items in flight.
-    int gather_row = -1;
-    float gather_next = 0.0f, gather_f[2] = {0.0f, 0.0f};
-    // panel and tile of the item that gather_row is for, advanced without the divisions of tile_at
-    const int step_panel = (int)(gridDim.x / ntiles), step_tile = (int)(gridDim.x - step_panel * ntiles);
-    int gather_panel = (int)(blockIdx.x / ntiles), gather_tile = (int)(blockIdx.x - gather_panel * ntiles);
-    auto advance = [&](int& panel, int& tile) {
-        panel += step_panel;
-        tile += step_tile;
-        if (tile >= ntiles) {
-            tile -= (int)ntiles;
-            ++panel;
-        }
-    };
-    auto gather_find = [&](int it) {
-        gather_row = -1;
-        gather_next = 0.0f;
-        if (it >= total) return;
-        const int p = __ldg(a.src + (int64_t)gather_panel * 128 + R0 + (cl & 7));
-        if (p < 0 || p >= a.x_rows * a.k) return;
-        gather_row = p / a.k;
-        gather_next = a.weight ? __ldg(a.weight + p) : 1.0f;
-    };
-    auto gather_issue = [&](int it) {
-        const uint32_t dst = smem_u32(stages + (it % STAGES) * PS::STAGE_BYTES) + R0 * 256 + C0 * 2;
-        const uint16_t* col = a.x + gather_tile * 128 + C0;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = __shfl_sync(0xffffffffu, gather_row, (lane & 16) | i);
-            cp_async_16(dst + 256 * i, r < 0 ? a.x : col + (int64_t)r * a.ldx, r < 0 ? 0u : 16u);
-        }
-        cp_async_commit();
-        gather_f[1] = gather_f[0];
-        gather_f[0] = gather_next;
-        advance(gather_panel, gather_tile);
-        gather_find(it + 1);
-    };
-    if (PRO == PRO_GATHER) {
-        static_assert(PRO != PRO_GATHER || STAGES == 2, "the factors of two items in flight");
-        gather_find(0);
-        for (; issued < STAGES; ++issued) gather_issue(issued);
-    } else if (tid == 0) {
+    if (tid == 0)
         for (; issued < STAGES && issued < total; ++issued) issue(issued);
-    }
     // every thread waits for item `it`; the decision to stop is made block-wide
     auto wait_item = [&](int it) -> bool {
-        if (PRO == PRO_GATHER) {
-            cp_async_wait_group<STAGES - 1>();
-            return true;
-        }
         const bool got = mbar_wait(smem_u32(&full_bar[it % STAGES]), (it / STAGES) & 1, a.timeout_ns, &abort_flag);
         return !__syncthreads_or(got ? 0 : 1);
     };
@@ -673,23 +620,15 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
         const int64_t m = pnl * 128 + R0 + (cl & 7);
         return m < a.M ? __ldg(a.xs + (tt + (cl < 8 ? 0 : ntiles / 2)) * a.M + m) : 0.0f;
     };
-    int at_panel = (int)(blockIdx.x / ntiles), at_tile = (int)(blockIdx.x - at_panel * ntiles);   // GATHER: of `item`
     float ck_next = 0.0f;
     if (PRO == PRO_SILU_BWD_CK && total > 0) ck_next = ckpt_scale(0);
     for (; ok && item < total; ++item) {
         const float ck_scale = ck_next;
-        const float gather_w = gather_f[1];      // of this item (the next one's is gather_f[0])
         if (PRO == PRO_SILU_BWD_CK && item + 1 < total) ck_next = ckpt_scale(item + 1);
         ok = wait_item(item);
         if (!ok) break;
         int64_t panel, t;
-        if (PRO == PRO_GATHER) {
-            panel = at_panel;
-            t = at_tile;
-            advance(at_panel, at_tile);
-        } else {
-            tile_at(item, panel, t);
-        }
+        tile_at(item, panel, t);
         const int64_t m0 = panel * 128;
         uint8_t* const stage = stages + (item % STAGES) * PS::STAGE_BYTES;
         // Quantize one output tile, column block tt, from this thread's BF16 words w (8 rows
@@ -736,9 +675,7 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             // double the registers and halve the CTAs per SM
             auto xrow = [&](int i, int j) { return make_float2(bf16_lo(w[i][j]), bf16_hi(w[i][j])); };
             __syncthreads();                                  // stage consumed, column maxima published
-            if (PRO == PRO_GATHER) {
-                gather_issue(issued++);
-            } else if (tid == 0 && issued < total) {
+            if (tid == 0 && issued < total) {
                 if (refill == 1) issue(issued++);
                 else if (refill == 2) issue(issued, 1);
             }
@@ -959,26 +896,13 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
             #pragma unroll
             for (int i = 0; i < 8; ++i)   // rows past M (TMA zero fill) are never stored
                 rg[i] = (PRO == PRO_RMSNORM_G && m0 + R0 + i < a.M) ? __ldg(a.rstd_out + m0 + R0 + i) : 0.0f;
-            rows_from_smem<PRO == PRO_GATHER ? PRO_COPY : PRO>(stage, a, t * 128, R0, C0, s_rstd, rg, w);
-            if (PRO == PRO_GATHER && a.weight) {
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float f = __shfl_sync(0xffffffffu, gather_w, (lane & 16) | i);
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 y = __fmul2_rn(make_float2(bf16_lo(w[i][j]), bf16_hi(w[i][j])), make_float2(f, f));
-                        w[i][j] = pack_bf16x2(y.x, y.y);
-                    }
-                }
-            }
+            rows_from_smem<PRO>(stage, a, t * 128, R0, C0, s_rstd, rg, w);
             // this tile's qT staging buffer (two, alternating: the next tile's barrier orders
             // this tile's reads before the writes of the tile after)
             quantize_tile(w, t, smem_u32(stages + PS::COLQ_OFF) + (uint32_t)(item & 1) * (128u * 128u), 1);
         }
     }
-    if (PRO == PRO_GATHER) {
-        cp_async_wait_all();
-    } else if (tid == 0) {
+    if (tid == 0) {
         // after an abort: let every issued copy land before the CTA exits
         for (int j = item; j < issued; ++j) {
             volatile int no_abort = 0;
@@ -988,6 +912,34 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
     if (PRO == PRO_RMSNORM) {
         // Keep this CTA's partial sums alive until every peer has read them.
         cg::this_cluster().sync();
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Rows of x in the order of the experts, each times its pair's weight where one is given and rounded
+// to BF16; rows of no pair are zeros.
+// ------------------------------------------------------------------------------------
+struct GatherArgs {
+    const uint16_t* x;      // [T][ldx]
+    int64_t ldx, T, K;
+    int k;
+    int64_t R;              // rows of the result; row r comes from pair p = src[r], row p / k of x, pair p goes to pos[p]
+    const int32_t* src;
+    const int32_t* pos;
+    const float* weight;    // [T][k], nullable
+    uint8_t* q;             // [R][K]
+    float* s;               // [K/128][R]
+    uint8_t* qT;            // [K][R]
+    float* sT;              // [R/128][K]
+    uint32_t k_mul;         // p / k = p k_mul >> k_shift for p < 2^30
+    int k_shift;
+};
+// A row's words times its factor.
+__device__ __forceinline__ void scale_row(uint32_t (&y)[4], const uint32_t (&w)[4], float f) {
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = __fmul2_rn(make_float2(bf16_lo(w[j]), bf16_hi(w[j])), make_float2(f, f));
+        y[j] = pack_bf16x2(v.x, v.y);
     }
 }
 
@@ -1003,12 +955,12 @@ __global__ void __launch_bounds__(256, 2) k_quant_panel(const __grid_constant__ 
 // ------------------------------------------------------------------------------------
 constexpr int scatter_blocks(bool weighted) { return weighted ? 4 : 8; }      // of an SM
 template <bool WEIGHTED>
-__global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(const PanelArgs a, const int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(const GatherArgs a) {
     grid_dependency_begin();
     const int lane = threadIdx.x & 31, half = lane >> 4, cl = lane & 15;
     const int R0 = 8 * half, C0 = 8 * cl;
     const int ntiles = (int)(a.K / 128);
-    const int64_t nrb = (a.x_rows + 15) / 16;
+    const int64_t nrb = (a.T + 15) / 16;
     const int64_t first = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), step = (int64_t)gridDim.x * 4;
     int64_t rb = first / ntiles;
     int ct = (int)(first - rb * ntiles);
@@ -1017,24 +969,25 @@ __global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(
     while (rb < nrb) {
         const int64_t t0 = rb * 16 + R0;
         const int64_t mine = t0 + (cl & 7);             // the token whose places this lane holds
-        const bool has = mine < a.x_rows;
+        const bool has = mine < a.T;
         uint32_t w[8][4];
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (t0 + i < a.x_rows) v = ldg_nc_v4(a.x + (t0 + i) * a.ldx + ct * 128 + C0);
+            if (t0 + i < a.T) v = ldg_nc_v4(a.x + (t0 + i) * a.ldx + ct * 128 + C0);
             w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
         }
         auto place = [&](int j) {
-            const int r = has ? __ldg(pos + mine * a.k + j) : -1;
-            return r >= 0 && r < a.M ? r : -1;
+            const int r = has ? __ldg(a.pos + mine * a.k + j) : -1;
+            return r >= 0 && r < a.R ? r : -1;
         };
         uint8_t* const q = a.q + ct * 128 + C0;
-        float* const s = a.s + (int64_t)ct * a.M;
+        float* const s = a.s + (int64_t)ct * a.R;
         if constexpr (!WEIGHTED) {
             uint32_t lo[8], hi[8];
             float sc = 0.0f;
-            encode_rows_8x8(w, lane, [&](float v) { sc = v; }, [&](int i, uint32_t l, uint32_t h) { lo[i] = l; hi[i] = h; });
+            encode_rows_8x8(w, row_maximum_8x8(w, lane), lane, [&](float v) { sc = v; },
+                            [&](int i, uint32_t l, uint32_t h) { lo[i] = l; hi[i] = h; });
             for (int j = 0; j < a.k; ++j) {
                 const int r = place(j);
                 if (r >= 0 && cl < 8) s[r] = sc;
@@ -1045,20 +998,19 @@ __global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(
                 }
             }
         } else {
+            // Rounding a product is monotone: the largest |w x| is |w| times the largest |x|, rounded the
+            // same way, while w is finite (an infinite one makes a NaN of a zero).  122 us at 65536 pairs x
+            // 4096; with maxima of their own for every copy 140.
+            const float largest = bf16_bits_amax_to_f32(row_maximum_8x8(w, lane));
             for (int j = 0; j < a.k; ++j) {
                 const int r = place(j);
                 const float f = r >= 0 ? __ldg(a.weight + mine * a.k + j) : 0.0f;
                 uint32_t y[8][4];
                 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float g = __shfl_sync(0xffffffffu, f, (lane & 16) | i);
-                    #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 v = __fmul2_rn(make_float2(bf16_lo(w[i][c]), bf16_hi(w[i][c])), make_float2(g, g));
-                        y[i][c] = pack_bf16x2(v.x, v.y);
-                    }
-                }
-                encode_rows_8x8(y, lane, [&](float v) { if (r >= 0 && cl < 8) s[r] = v; },
+                for (int i = 0; i < 8; ++i) scale_row(y[i], w[i], __shfl_sync(0xffffffffu, f, (lane & 16) | i));
+                uint32_t m = pack_bf16x2(__fmul_rn(fabsf(f), largest), 0.0f) & 0x7FFFu;
+                if (__any_sync(0xffffffffu, !(fabsf(f) < INFINITY))) m = row_maximum_8x8(y, lane);
+                encode_rows_8x8(y, m, lane, [&](float v) { if (r >= 0 && cl < 8) s[r] = v; },
                                 [&](int i, uint32_t l, uint32_t h) {
                                     const int ri = __shfl_sync(0xffffffffu, r, (lane & 16) | i);
                                     if (ri >= 0) stg_v2(q + (int64_t)ri * a.K, l, h);
@@ -1073,14 +1025,128 @@ __global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(
         }
     }
     // rows of no pair: they come in runs, so neighbouring rows go to different warps
-    for (int64_t r0 = first; r0 < a.M; r0 += step * 32) {
+    for (int64_t r0 = first; r0 < a.R; r0 += step * 32) {
         const int64_t mine = r0 + lane * step;
-        const int p = mine < a.M ? __ldg(a.src + mine) : 0;
-        for (uint32_t none = __ballot_sync(0xffffffffu, p < 0 || p >= a.x_rows * a.k); none; none &= none - 1) {
+        const int p = mine < a.R ? __ldg(a.src + mine) : 0;
+        for (uint32_t none = __ballot_sync(0xffffffffu, p < 0 || p >= a.T * a.k); none; none &= none - 1) {
             const int64_t r = r0 + (__ffs(none) - 1) * step;
             for (int64_t c = lane * 16; c < a.K; c += 512) *reinterpret_cast<uint4*>(a.q + r * a.K + c) = make_uint4(0, 0, 0, 0);
-            for (int c = lane; c < ntiles; c += 32) a.s[(int64_t)c * a.M + r] = 0.0f;
+            for (int c = lane; c < ntiles; c += 32) a.s[(int64_t)c * a.R + r] = 0.0f;
         }
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Rows of x in expert order quantized 128x1 (qT, sT).  A warp takes 128 rows x 32 columns by itself:
+// lane 4 rl + cq has rows 16 rl .. 16 rl + 15 and columns 8 cq .. 8 cq + 7, so a column's 16 codes are
+// one 16-byte store, eight lanes' a line of qT, and nothing waits for another warp.  The next strip is
+// copied to shared memory while this one is encoded (without that 137 us for 107 at 65536 pairs x
+// 4096, 0.75 of the copy rate by the 537 MB that L2 gives and the 277 MB written; the panel kernels'
+// tiles of 128 x 128, their columns' maxima and codes put together in shared memory, took 204).  Bound by
+// the encode's chains, at 16 warps an SM: 96 registers and 20 warps spill and take 112.
+// ------------------------------------------------------------------------------------
+constexpr int kColsStrips = 2;      // strips of 32 columns of a warp: its rows' sources are looked up once
+template <bool WEIGHTED>
+__global__ void __launch_bounds__(128, 4) k_gather_cols(const GatherArgs a) {
+    __shared__ uint4 s_piece[4][16][32];
+    grid_dependency_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rl = lane >> 2, cq = lane & 3;
+    const int64_t m0 = (int64_t)blockIdx.x * 128;
+    const int strips = (int)(a.K / 32);
+    // lane l: the sources of rows 4 l .. 4 l + 3 (-1: none) and their factors
+    int tok[4];
+    float wt[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = __ldg(a.src + m0 + 4 * lane + i);
+        const bool has = p >= 0 && p < a.T * a.k;
+        tok[i] = has ? (int)(((uint64_t)(uint32_t)p * a.k_mul) >> a.k_shift) : -1;
+        wt[i] = WEIGHTED && has ? __ldg(a.weight + p) : 0.0f;
+    }
+    // the lane's pieces of the next strip, copied while this one is encoded: a lane reads back its own
+    // alone
+    const uint32_t piece = smem_u32(s_piece[warp][0] + lane);
+    auto request = [&](int strip) {
+        const uint16_t* const col = a.x + strip * 32 + cq * 8;
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = __shfl_sync(0xffffffffu, tok[i & 3], 4 * rl + (i >> 2));
+            cp_async_16(piece + 512 * i, r < 0 ? a.x : col + (int64_t)r * a.ldx, r < 0 ? 0u : 16u);
+        }
+        cp_async_commit();
+    };
+    // strips of this warp: the chunk's, then those of the chunk gridDim.y on
+    int u = 0, chunk = (int)blockIdx.y;
+    auto strip_at = [&] { return (chunk * kColsStrips + u) * 4 + warp; };
+    int strip = strip_at();
+    if (strip < strips) request(strip);
+    #pragma unroll 1
+    while (strip < strips) {
+        if (++u == kColsStrips) {
+            u = 0;
+            chunk += (int)gridDim.y;
+        }
+        const int next = strip_at();
+        cp_async_wait_all();
+        uint32_t w[16][4];
+        #pragma unroll
+        for (int i = 0; i < 16; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(piece + 512 * i)
+                         : "memory");
+        if (WEIGHTED) {
+            #pragma unroll
+            for (int i = 0; i < 16; ++i) scale_row(w[i], w[i], __shfl_sync(0xffffffffu, wt[i & 3], 4 * rl + (i >> 2)));
+        }
+        // column maxima: over the lane's rows, then over the lanes of its columns, each step halving
+        // what a lane keeps: in the end the maximum of column rl of its eight
+        uint32_t m[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = 0u;
+            #pragma unroll
+            for (int i = 0; i < 16; ++i) m[j] = absmax2(m[j], w[i][j]);
+        }
+        const bool b4 = lane & 16, b3 = lane & 8;
+        #pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, b4 ? m[j] : m[2 + j], 16);
+            m[j] = __vmaxu2(b4 ? m[2 + j] : m[j], o);
+        }
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, b3 ? m[0] : m[1], 8);
+        m[0] = __vmaxu2(b3 ? m[1] : m[0], o);
+        m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 4));
+        if (next < strips) request(next);      // the maxima needed every piece of this one
+        const FastScale fs = fast_scale(bf16_bits_amax_to_f32((lane & 4) ? m[0] >> 16 : m[0] & 0xFFFFu));
+        a.sT[(int64_t)blockIdx.x * a.K + strip * 32 + cq * 8 + rl] = fs.s;
+        uint8_t* const out = a.qT + (int64_t)(strip * 32 + cq * 8) * a.R + m0 + 16 * rl;
+        #pragma unroll
+        for (int cc = 0; cc < 8; ++cc) {
+            const int j = cc >> 1;
+            const float s = __shfl_sync(0xffffffffu, fs.s, 4 * cc + cq);
+            const float nr = __shfl_sync(0xffffffffu, fs.nr, 4 * cc + cq);
+            const uint32_t keep = s == 0.0f ? 0u : 0xFFFFFFFFu;
+            auto x = [&](int k) {      // rows 2k, 2k + 1
+                return (cc & 1) ? make_float2(bf16_hi_v(w[2 * k][j]), bf16_hi_v(w[2 * k + 1][j]))
+                                : make_float2(bf16_lo_v(w[2 * k][j]), bf16_lo_v(w[2 * k + 1][j]));
+            };
+            uint32_t c[4];
+            #pragma unroll
+            for (int q = 0; q < 4; ++q)
+                c[q] = flip_codes(encode_pair_neg(x(2 * q), s, nr), encode_pair_neg(x(2 * q + 1), s, nr), keep);
+            if (s > 0.0f && scale_is_slow(s)) {
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 v = encode4_slow(x(4 * h), x(4 * h + 1), x(4 * h + 2), x(4 * h + 3), s);
+                    c[2 * h] = v.x | (v.y << 16);
+                    c[2 * h + 1] = v.z | (v.w << 16);
+                }
+            }
+            stg_v4(out + (int64_t)cc * a.R, c[0], c[1], c[2], c[3]);
+        }
+        strip = next;
     }
 }
 
@@ -1359,8 +1425,7 @@ template <int PRO, bool ROW_OUT, bool COL_OUT>
 static cudaError_t launch_panel_t(const PanelArgs& a, int64_t in_cols, int cluster, cudaStream_t st) {
     CUtensorMap tm, tm2;
     constexpr bool pair = PRO == PRO_SILU_BWD || PRO == PRO_SILU_BWD_CK;
-    cudaError_t e = PRO == PRO_DEQUANT || PRO == PRO_SILU_BWD_CK ? tmap_u8(&tm, a.x, a.M, in_cols)
-                    : tmap_bf16(&tm, a.x, PRO == PRO_GATHER ? a.x_rows : a.M, in_cols, a.ldx);
+    cudaError_t e = PRO == PRO_DEQUANT || PRO == PRO_SILU_BWD_CK ? tmap_u8(&tm, a.x, a.M, in_cols) : tmap_bf16(&tm, a.x, a.M, in_cols, a.ldx);
     if (e != cudaSuccess) return e;
     if (pair) {
         e = tmap_bf16(&tm2, a.x2, a.M, a.K / 2, a.K / 2);
@@ -1419,21 +1484,22 @@ cudaError_t launch_quant_dual(const uint16_t* x, int64_t M, int64_t K, int64_t l
 
 // rows of x in expert order, each times its pair's weight, quantized 1x128 and (qT) 128x1
 cudaError_t launch_expert_gather(const uint16_t* x, int64_t ldx, int64_t K, const float* weight, const fp8rl_expert_layout& l,
-                                 uint8_t* q, float* s, uint8_t* qT, float* sT, int num_sms, uint64_t timeout_ns,
-                                 cudaStream_t st) {
-    PanelArgs a = {};
-    a.x = x; a.ldx = ldx; a.M = l.R; a.K = K; a.q = q; a.s = s; a.qT = qT; a.sT = sT;
-    a.src = l.src; a.weight = weight; a.x_rows = l.T; a.k = (int)l.k;
-    a.timeout_ns = timeout_ns;
-    // Both layouts.  With weights every copy of a row is encoded by itself: one pass in expert order for
-    // rows and columns (65536 pairs x 4096: 315 us, against 363 in two).  Without, the rows token by
-    // token and the columns in expert order (280 us, against 291 in one).
-    if (qT && weight) return launch_panel_t<PRO_GATHER, true, true>(a, K, 0, st);
+                                 uint8_t* q, float* s, uint8_t* qT, float* sT, int num_sms, cudaStream_t st) {
+    GatherArgs a = {};
+    a.x = x; a.ldx = ldx; a.T = l.T; a.K = K; a.k = (int)l.k; a.R = l.R; a.src = l.src; a.pos = l.pos; a.weight = weight;
+    a.q = q; a.s = s; a.qT = qT; a.sT = sT;
+    // 2^n / k, n = 30 + ceil(log2 k), rounded up: the excess adds less than p / 2^n < 1 / k to p / k
+    a.k_shift = 30;
+    while ((1 << (a.k_shift - 30)) < a.k) ++a.k_shift;
+    a.k_mul = (uint32_t)((uint64_t(1) << a.k_shift) / (uint64_t)a.k + 1);
     const int64_t items = (l.T + 15) / 16 * (K / 128);
     const int64_t blocks = std::min<int64_t>((items + 3) / 4, (int64_t)num_sms * scatter_blocks(weight != nullptr));
     const cudaError_t e = launch_dependent(weight ? k_scatter_rows<true> : k_scatter_rows<false>, dim3((unsigned)blocks), dim3(128), 0,
-                                           st, a, l.pos);
-    return e != cudaSuccess || !qT ? e : launch_panel_t<PRO_GATHER, false, true>(a, K, 0, st);
+                                           st, a);
+    if (e != cudaSuccess || !qT) return e;
+    const int64_t chunks = (K + 128 * kColsStrips - 1) / (128 * kColsStrips);
+    const dim3 grid((unsigned)(l.R / 128), (unsigned)std::min<int64_t>(chunks, 65535));
+    return launch_dependent(weight ? k_gather_cols<true> : k_gather_cols<false>, grid, dim3(128), 0, st, a);
 }
 
 cudaError_t launch_silu_mul_quant(const uint16_t* gu, int64_t M, int64_t I, uint8_t* q, float* s,

@@ -304,6 +304,64 @@ def test_gather_keeps_nan_and_infinity_of_other_tokens_out(fp8lib, oracle):
     assert np.array_equal(qT.cpu().numpy()[:, lo:hi], c[0])
 
 
+def test_gather_of_groups_next_to_zero(fp8lib, oracle):
+    """Groups whose scale is below 2^-68 or subnormal, or whose products underflow, beside ordinary ones."""
+    T, E, k, K = 260, 3, 2, 256
+    idx = draw_index(T, E, k, 5, 0)
+    rows = fp8lib.expert_rows(torch.tensor(idx, device=DEV), E)
+    x = synth.normal_bf16((T, K), 1.0, 3, torch.device(DEV)).float()
+    x[:, :40] *= 2.0 ** -70
+    x[:, 128:] *= 2.0 ** -75
+    x[7:9] *= 2.0 ** -60
+    x[11] = 0
+    x = x.to(torch.bfloat16)
+    for w in (None, torch.randn((T, k), device=DEV) * 2.0 ** torch.randint(-60, 3, (T, k), device=DEV)):
+        src = ints(rows.src)
+        v = torch.zeros((len(src), K), dtype=torch.bfloat16, device=DEV)
+        has = torch.tensor(src >= 0, device=DEV)
+        p = torch.tensor(src, device=DEV)[has]
+        v[has] = x[p // k] if w is None else (x[p // k].float() * w.reshape(-1)[p][:, None]).to(torch.bfloat16)
+        quant_same(oracle, fp8lib.expert_gather_quant(x, rows, w, dual=True), bits(v), True)
+
+
+def test_gather_weights_that_are_no_numbers(fp8lib):
+    """An infinite or missing weight, an infinite or missing input: the scales tell, other rows stay as they are."""
+    T, K = 40, 256
+    idx = torch.randint(0, 4, (T, 1), dtype=torch.int32, device=DEV)
+    rows = fp8lib.expert_rows(idx, 4, 1)
+    x = synth.normal_bf16((T, K), 1.0, 7, torch.device(DEV))
+    w = torch.randn((T, 1), device=DEV)
+    x[3, 5], x[4, 6], x[5, 200], x[9, 130] = float("inf"), float("nan"), 0, 0
+    w[5], w[6], w[7], w[3], w[4] = float("inf"), float("nan"), float("inf"), 0, 0
+    x[7] = 1
+    q, s, _, _ = fp8lib.expert_gather_quant(x, rows, w)
+    y = (x.float() * w).to(torch.bfloat16)
+    q1, s1, _, _ = fp8lib.expert_gather_quant(y, rows)
+    bad = ~torch.isfinite(s1)
+    assert bad.any(0).sum() == 5
+    assert torch.equal(torch.isnan(s), torch.isnan(s1)) and torch.equal(s[~torch.isnan(s)], s1[~torch.isnan(s1)])
+    same = ~bad.t().repeat_interleave(128, 1)
+    assert torch.equal(q[same], q1[same])
+
+
+def test_gather_by_an_order_at_any_offset(fp8lib, oracle):
+    """The arrays of an order need the alignment of their elements alone."""
+    T, E, k, K = 150, 5, 3, 256
+    rows = fp8lib.expert_rows(torch.tensor(draw_index(T, E, k, 2, 0.1), device=DEV), E)
+
+    def moved(t, by):
+        b = torch.empty(t.numel() + by, dtype=t.dtype, device=DEV)
+        b[by:] = t.reshape(-1)
+        return b[by:].view(t.shape)
+
+    x = synth.normal_bf16((T, K), 1.0, 7, torch.device(DEV))
+    w = moved(torch.randn((T, k), device=DEV), 1)
+    want = fp8lib.expert_gather_quant(x, rows, w, dual=True)
+    for by in (1, 2, 3):
+        odd = fp8lib.ExpertRows(*(moved(t, by) for t in rows[:4]), rows.align)
+        assert all(torch.equal(a, b) for a, b in zip(fp8lib.expert_gather_quant(x, odd, w, dual=True), want))
+
+
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("T,E,k,N,align,res,missing", [
     (1, 64, 8, 128, 1, False, 0), (61, 64, 6, 1000, 1, True, 0), (300, 8, 3, 384, 128, True, 0.2), (5, 4, 2, 8, 1, False, 1.0),
