@@ -782,16 +782,15 @@ def expert_rows(index: torch.Tensor, n_experts: int, align: int = 128) -> Expert
     (T, k), E, align, dev = index.shape, int(n_experts), int(align), index.device
     L = lib()
     R = L.fp8rl_expert_rows_capacity(T, k, E, align)
-    n = E if E > 0 else 0
-    # the four arrays in one allocation
-    buf = torch.empty(R + 2 * n + 1 + T * k, dtype=torch.int32, device=dev)
-    src, start = buf.as_strided((R,), (1,), 0), buf.as_strided((n + 1,), (1,), R)
-    count, pos = buf.as_strided((n,), (1,), R + n + 1), buf.as_strided((T, k), (k, 1), R + 2 * n + 1)
+    # (views of one allocation took 2.5 us longer)
+    src = torch.empty(R, dtype=torch.int32, device=dev)
+    start = torch.empty(E + 1 if E > 0 else 1, dtype=torch.int32, device=dev)
+    count = torch.empty(E if E > 0 else 0, dtype=torch.int32, device=dev)
+    pos = torch.empty((T, k), dtype=torch.int32, device=dev)
     need = L.fp8rl_expert_rows_workspace_bytes(T, k, E)
     # a buffer of this call's own: calls may run on several streams
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    at = buf.data_ptr()
-    l = _abi.ExpertLayout(at + 4 * (R + 2 * n + 1), at, at + 4 * R, at + 4 * (R + n + 1), T, k, E, R, align)
+    l = _abi.ExpertLayout(pos.data_ptr(), src.data_ptr(), start.data_ptr(), count.data_ptr(), T, k, E, R, align)
     check(L.fp8rl_expert_rows(index.data_ptr(), T, k, E, align, l.pos, l.src, l.start, l.count, _ptr(ws), need,
                               _stream(dev)), "fp8rl_expert_rows")
     rows = _SortedRows(pos, src, start, count, align)
