@@ -1040,11 +1040,18 @@ __global__ void __launch_bounds__(128, scatter_blocks(WEIGHTED)) k_scatter_rows(
 // Rows of x in expert order quantized 128x1 (qT, sT).  A warp takes 128 rows x 32 columns by itself:
 // lane 4 rl + cq has rows 16 rl .. 16 rl + 15 and columns 8 cq .. 8 cq + 7, so a column's 16 codes are
 // one 16-byte store, eight lanes' a line of qT, and nothing waits for another warp.  The next strip is
-// copied to shared memory while this one is encoded (without that 137 us for 107 at 65536 pairs x
-// 4096, 0.75 of the copy rate by the 537 MB that L2 gives and the 277 MB written; the panel kernels'
-// tiles of 128 x 128, their columns' maxima and codes put together in shared memory, took 204).  Bound by
-// the encode's chains, at 16 warps an SM: 96 registers and 20 warps spill and take 112.
+// copied to shared memory while this one is encoded (without that 33 us more: 102 at 65536 pairs x
+// 4096; the panel kernels' tiles of 128 x 128, their columns' maxima and codes put together in shared
+// memory, took 204).  Bound by its instructions, 7.5 an element, at 52% of the issue slots and 51% of the
+// ALU pipe with 16 warps an SM; 96 registers and 20 warps spill and took 7 us longer.
 // ------------------------------------------------------------------------------------
+// The larger magnitude of packed BF16 pairs, NaN if either is one: one instruction where the integers'
+// way takes two.
+__device__ __forceinline__ uint32_t absmax2_bf16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 constexpr int kColsStrips = 2;      // strips of 32 columns of a warp: its rows' sources are looked up once
 template <bool WEIGHTED>
 __global__ void __launch_bounds__(128, 4) k_gather_cols(const GatherArgs a) {
@@ -1072,7 +1079,7 @@ __global__ void __launch_bounds__(128, 4) k_gather_cols(const GatherArgs a) {
         #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int r = __shfl_sync(0xffffffffu, tok[i & 3], 4 * rl + (i >> 2));
-            cp_async_16(piece + 512 * i, r < 0 ? a.x : col + (int64_t)r * a.ldx, r < 0 ? 0u : 16u);
+            cp_async_16(piece + 512 * i, col + (int64_t)max(r, 0) * a.ldx, r < 0 ? 0u : 16u);
         }
         cp_async_commit();
     };
@@ -1107,7 +1114,7 @@ __global__ void __launch_bounds__(128, 4) k_gather_cols(const GatherArgs a) {
         for (int j = 0; j < 4; ++j) {
             m[j] = 0u;
             #pragma unroll
-            for (int i = 0; i < 16; ++i) m[j] = absmax2(m[j], w[i][j]);
+            for (int i = 0; i < 16; ++i) m[j] = absmax2_bf16(m[j], w[i][j]);
         }
         const bool b4 = lane & 16, b3 = lane & 8;
         #pragma unroll
@@ -1121,6 +1128,7 @@ __global__ void __launch_bounds__(128, 4) k_gather_cols(const GatherArgs a) {
         if (next < strips) request(next);      // the maxima needed every piece of this one
         const FastScale fs = fast_scale(bf16_bits_amax_to_f32((lane & 4) ? m[0] >> 16 : m[0] & 0xFFFFu));
         a.sT[(int64_t)blockIdx.x * a.K + strip * 32 + cq * 8 + rl] = fs.s;
+        const bool any_slow = __any_sync(0xffffffffu, fs.slow);
         uint8_t* const out = a.qT + (int64_t)(strip * 32 + cq * 8) * a.R + m0 + 16 * rl;
         #pragma unroll
         for (int cc = 0; cc < 8; ++cc) {
@@ -1136,7 +1144,7 @@ __global__ void __launch_bounds__(128, 4) k_gather_cols(const GatherArgs a) {
             #pragma unroll
             for (int q = 0; q < 4; ++q)
                 c[q] = flip_codes(encode_pair_neg(x(2 * q), s, nr), encode_pair_neg(x(2 * q + 1), s, nr), keep);
-            if (s > 0.0f && scale_is_slow(s)) {
+            if (any_slow && s > 0.0f && scale_is_slow(s)) {
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint4 v = encode4_slow(x(4 * h), x(4 * h + 1), x(4 * h + 2), x(4 * h + 3), s);
