@@ -45,7 +45,10 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_hist(const int32_t* 
 // Places one block's pairs.  Each warp has a contiguous part of them: the warps' counts, summed over
 // the warps and blocks before, give every warp its first row of each expert, and within 32 pairs
 // match_any ranks the pairs of one expert by lane, so the order is that of the pairs.
-// s_n: [kSortWarps][E] counts, then first rows; s_start [E + 1].
+// s_n: [kSortWarps][E] counts, then first rows; s_start [E + 1]; s_count [E]; s_warp [kSortWarps].  All of it
+// is the launch's own (place_smem): static arrays beside it would count towards the 48 KB that a launch has
+// without asking.
+constexpr size_t place_smem(int64_t E) { return ((size_t)(kSortWarps + 2) * E + 1 + kSortWarps) * 4; }
 __global__ void __launch_bounds__(32 * kSortWarps) k_expert_place(const int32_t* __restrict__ index, int64_t P, int E,
                                                                   int64_t chunk, int align, int64_t R,
                                                                   const int32_t* __restrict__ hist, int32_t* __restrict__ pos,
@@ -55,7 +58,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_place(const int32_t*
     grid_dependency_begin();
     int32_t* const s_start = s_n + kSortWarps * E;
     int32_t* const s_count = s_start + E + 1;
-    __shared__ int32_t s_warp[kSortWarps];
+    int32_t* const s_warp = s_count + E;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nb = gridDim.x, b = blockIdx.x;
     for (int i = tid; i < kSortWarps * E; i += blockDim.x) s_n[i] = 0;
@@ -240,10 +243,10 @@ cudaError_t launch_expert_rows(const int32_t* index, int64_t P, int E, int align
         const cudaError_t e = launch_dependent(k_expert_hist, dim3(nb), dim3(32 * kSortWarps), (size_t)E * 4, st, index, P, E, chunk, hist);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = ((size_t)kSortWarps * E + 2 * E + 1) * 4;
+    const size_t smem = place_smem(E);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)(((size_t)kSortWarps + 2) * kMaxExperts * 4 + 4));
+                                                   (int)place_smem(kMaxExperts));
         if (e != cudaSuccess) return e;
     }
     return launch_dependent(k_expert_place, dim3(nb), dim3(32 * kSortWarps), smem, st, index, P, E, chunk, align, R, hist, pos, src,
