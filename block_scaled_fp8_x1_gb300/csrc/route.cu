@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const fp8rl_route_ar
 // t = sum p + 1e-20,
 //     ds_j = c g_j,  or renormalised  c (g_j - sum_i g_i p_i / t) / t,
 //     sigmoid  dz_e = s_e (1 - s_e) ds_e,     softmax  dz_e = s_e (ds_e - sum_j ds_j p_j),
-// where the last sum is 0 for renormalised weights (which do not change with the sum over all).
+// where the last sum is c (sum_i g_i p_i / t) 1e-20 / t for renormalised weights: they change with the sum over
+// all scores only as far as t is not far above the 1e-20.
 template <int NL, bool BF16>
 __global__ void __launch_bounds__(32 * kRouteWarps) k_route_bwd(const fp8rl_route_bwd_args a, int64_t T, int E) {
     const int lane = threadIdx.x & 31;
@@ -608,6 +609,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route_bwd(const fp8rl_rout
         const float t = warp_sum(p) + kTiny;
         const float mean = warp_sum(g * p) / t;
         g = idx >= 0 ? (g - mean) / t : 0.0f;
+        // (above 1e-12 less than half a unit of the other terms: left out, so that experts that were not
+        // chosen keep a gradient of 0)
+        if (sm && t < 1e-12f) inner = mean * (kTiny / t);
     } else if (sm) {
         inner = warp_sum(g * p);
     }

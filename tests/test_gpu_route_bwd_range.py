@@ -1,4 +1,4 @@
-"""route_topk_bwd where scores end: logits far from zero.
+"""route_topk_bwd where scores end: logits far from zero, chosen scores next to nothing.
 
 The sigmoid's derivative is s (1 - s).  Bound: the scores' and the exponential's FP32 roundings and the sum of
 k weights, 2^-16 of (the largest |gradient of a weight| over the sum) times s (1 - s), each in 64 bits; half
@@ -62,3 +62,29 @@ def test_sigmoid_ends_in_zero_not_in_nan(fp8lib):
     index = torch.arange(7, dtype=torch.int32, device=DEV)[None]
     d = fp8lib.route_topk_bwd(torch.ones((1, 7), device=DEV), z, index, score="sigmoid", renormalize=False)
     assert d.tolist() == [[0.0] * 6 + [0.25]]
+
+
+@pytest.mark.parametrize("below", [20.0, 35.0, 46.0, 48.0, 60.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_chosen_scores_next_to_nothing(fp8lib, score, below):
+    """A bias can choose experts whose scores are `e^-below` of the row's: where their sum is no longer far above
+    the 1e-20 that is added to it, the weights do change with the scores of all experts.
+
+    Bound: s_e (|ds_e| + sum s |ds|), the magnitudes that are added, times 2^-16: FP32 scores at a distance of
+    `below` are within 2^-18 of themselves."""
+    T, E, k = 16, 40, 3
+    gen = torch.Generator(DEV).manual_seed(int(below))
+    z = torch.randn((T, E), generator=gen, device=DEV)
+    z[:, :10] -= below
+    index = torch.stack([torch.randperm(10, generator=gen, device=DEV)[:k] for _ in range(T)]).to(torch.int32)
+    dw = 1.0 + torch.rand((T, k), generator=gen, device=DEV)
+    got = np64(fp8lib.route_topk_bwd(dw, z, index, score=score, scale=1.5))
+    z64, i = np64(z), index.cpu().numpy()
+    want = ref.route_bwd(np64(dw), z64, i, score, True, 1.5)
+    s = ref.scores(z64, score)
+    p = np.take_along_axis(s, i, 1)
+    total = p.sum(1, keepdims=True) + ref.TINY
+    ds = np.zeros((T, E))
+    np.put_along_axis(ds, i, 1.5 * (np64(dw) + (np64(dw) * p).sum(1, keepdims=True) / total) / total, 1)
+    size = s * (ds + (s * ds).sum(1, keepdims=True))
+    assert np.all(np.abs(got - want) <= 2.0 ** -16 * size)
