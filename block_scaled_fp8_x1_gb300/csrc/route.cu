@@ -7,8 +7,8 @@
 //     the k largest v among them, largest first, the lowest index first among equals,
 //     weight_j = scale s_j / (sum_j s_j + 1e-20)  or  scale s_j.
 //
-// The selection is that of the scores themselves, to 2^-40: a token's experts do not change with the
-// batch or with the last bits of an FP32 score.  Without a bias and with group_rank 1 the logits
+// The selection is that of the scores themselves, to 2^-40 (sums with a bias: or 2^-44 of the largest of them): a
+// token's experts do not change with the batch or with the last bits of an FP32 score.  Without a bias and with group_rank 1 the logits
 // themselves are compared (both scores are increasing functions of them).  Otherwise the FP32 scores
 // decide where they can (score_error), and where two neighbours of the order, or the groups' border,
 // are too close for that, those few scores are formed again in pairs of FP32.
@@ -181,24 +181,30 @@ __device__ __forceinline__ Pair key_pair(uint64_t k) {
 
 __device__ __forceinline__ uint64_t key_sum(uint64_t a, uint64_t b) { return order_key64(key_pair(a) + key_pair(b)); }
 
-// The warp's largest of b1 over the lanes, or the key of the sum of its two largest values (each lane
-// holding its own two best).
+// The warp's largest of b1 over the lanes and, with rank 2, the next one (each lane holding its own two
+// best; 0: none).
 template <typename KEY>
-__device__ __forceinline__ KEY two_best(KEY b1, KEY b2, int rank, int lane) {
-    KEY t = reduce_max(b1);
+__device__ __forceinline__ KEY two_best(KEY b1, KEY b2, int rank, int lane, KEY* second) {
+    const KEY t = reduce_max(b1);
+    *second = 0;
     if (rank == 2) {
         const uint32_t holder = __ballot_sync(kFull, b1 == t);
-        const KEY second = reduce_max(lane == __ffs(holder) - 1 ? b2 : b1);
-        if (second != 0) t = key_sum(t, second);
+        *second = reduce_max(lane == __ffs(holder) - 1 ? b2 : b1);
     }
     return t;
 }
 
+// The larger magnitude of two keys' values.
+__device__ __forceinline__ float key_size(uint32_t a, uint32_t b) { return fmaxf(fabsf(key_value(a)), fabsf(key_value(b))); }
+
 // Lane g gets the rank of group g: the largest key of its experts, or the key of the two largest
-// values' sum (0: no expert to select).
-template <int NL, typename KEY>
-__device__ __forceinline__ KEY group_scores(const fp8rl_route_args& a, int E, uint32_t gs_mul, int lane, const KEY (&key)[NL]) {
+// values' sum (0: no expert to select).  `addend`: the largest magnitude that a lane saw in such a sum.
+template <int NL>
+__device__ __forceinline__ uint32_t group_scores(const fp8rl_route_args& a, int E, uint32_t gs_mul, int lane, const uint32_t (&key)[NL],
+                                                 float* addend) {
+    using KEY = uint32_t;
     const int G = a.n_groups, gs = E / G;
+    *addend = 0.0f;
     const int lpg = gs / NL;                            // lanes of a group
     if (gs % NL == 0 && (lpg & (lpg - 1)) == 0) {
         // every group is lpg neighbouring lanes: its two best in log2(lpg) exchanges
@@ -213,7 +219,10 @@ __device__ __forceinline__ KEY group_scores(const fp8rl_route_args& a, int E, ui
             b2 = max(max(b2, o2), min(b1, o1));
             b1 = max(b1, o1);
         }
-        if (a.group_rank == 2 && b2 != 0) b1 = key_sum(b1, b2);
+        if (a.group_rank == 2 && b2 != 0) {
+            *addend = key_size(b1, b2);
+            b1 = key_sum(b1, b2);
+        }
         return __shfl_sync(kFull, b1, (lane * lpg) & 31);
     }
     KEY score = 0;
@@ -225,7 +234,12 @@ __device__ __forceinline__ KEY group_scores(const fp8rl_route_args& a, int E, ui
             b2 = max(b2, min(b1, k));
             b1 = max(b1, k);
         }
-        const KEY t = two_best(b1, b2, a.group_rank, lane);
+        KEY second;
+        KEY t = two_best(b1, b2, a.group_rank, lane, &second);
+        if (second != 0) {
+            *addend = fmaxf(*addend, key_size(t, second));
+            t = key_sum(t, second);
+        }
         if (lane == g) score = t;
     }
     return score;
@@ -322,7 +336,9 @@ __device__ __noinline__ uint32_t settle_groups(const Fine<BF16>& x, uint32_t uns
             b2 = max(b2, min(b1, k));
             b1 = max(b1, k);
         }
-        const uint64_t t = two_best(b1, b2, x.a.group_rank, lane);
+        uint64_t second;
+        uint64_t t = two_best(b1, b2, x.a.group_rank, lane, &second);
+        if (second != 0) t = key_sum(t, second);
         if (lane == g) score = t;
     }
     return best_lanes(score, (unsure >> lane) & 1u, n, lane);
@@ -482,14 +498,19 @@ __global__ void __launch_bounds__(32 * kRouteWarps) k_route(const fp8rl_route_ar
     };
     uint32_t keep = kFull;
     if (a.n_groups > 1) {
-        const uint32_t score = group_scores<NL, uint32_t>(a, E, gs_mul, lane, key);
+        float addend;
+        const uint32_t score = group_scores<NL>(a, E, gs_mul, lane, key, &addend);
         keep = best_lanes(score, lane < a.n_groups, a.top_groups, lane);
         const bool kept = (keep >> lane) & 1u;
         const uint32_t worst = ~__reduce_max_sync(kFull, kept ? ~score : 0u);
         const uint32_t left = __reduce_max_sync(kFull, !kept && lane < a.n_groups ? score : 0u);
         if (!by_logit && left != 0) {
-            // sums of two: twice the error on each side, and their own rounding
-            const float v = key_value(worst), margin = 6.0f * score_error(v, smax, sm);
+            // sums of two: twice the error on each side, and their own rounding; each of the two was rounded at
+            // its own size, which with biases of both signs is more than the sum's (without a bias no more
+            // than smax).  NaN and infinity let nothing pass.
+            const float v = key_value(worst);
+            float margin = 6.0f * score_error(v, smax, sm);
+            if (a.bias && a.group_rank == 2) margin += 0x1.8p-22f * __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(addend)));
             if (!(v - key_value(left) > margin)) {
                 // groups far enough above the best one left are in, those far below the worst kept out
                 const float own = key_value(score);

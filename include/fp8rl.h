@@ -541,8 +541,8 @@ typedef struct {
  * v = s + bias (the logits themselves where there is neither a bias nor a group_rank of 2, which
  * gives the same order); among the experts of the top_groups best groups the k largest v, largest
  * first, the lowest index first among equals.  The order is that of the scores themselves, to
- * 2^-40: those too close for FP32 are formed again in pairs of FP32.  weight = scale s / (sum of the
- * k s + 1e-20), or scale s.
+ * 2^-40, or 2^-44 of the largest |s + bias| where that is more: those too close for FP32 are formed
+ * again in pairs of FP32.  weight = scale s / (sum of the k s + 1e-20), or scale s.
  *   An expert whose logit or bias is -inf is never chosen; where fewer than k can be, the rest of
  *   the row has index -1 and weight 0 (a padding token is a row of -inf).  NaN ranks above every
  *   number, so that it shows in the weights.
