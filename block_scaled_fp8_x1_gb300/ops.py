@@ -877,7 +877,7 @@ def _expert_weights(q, s, shape, N: int, K: int, E: int, dev) -> None:
 
 
 def _divided(n: int, E: int, name: str) -> int:
-    if n % E != 0:
+    if E < 1 or n % E != 0:
         raise ValueError(f"{name}: {n} rows do not divide among {E} experts")
     return n // E
 
