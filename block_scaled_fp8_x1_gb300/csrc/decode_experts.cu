@@ -9,9 +9,10 @@
 // Work: items (unit, weight tile), a unit being up to MP rows of one expert.  A CTA takes half of an
 // SM's shared memory and registers.  Two CTAs an SM walk the items with one continuous copy / MMA /
 // epilogue pipeline each: a CTA's start (about 5 us from launch to its first sums: the counts,
-// tensor memory, the first copies) is paid once, not per item (1472 items of 11 K-blocks: 45 us one
-// a CTA, 38 this way).  Where the items are fewer than the SMs, a cluster of S CTAs shares each item's
-// reduction instead and adds its FP32 sums in rank order through distributed shared memory.
+// tensor memory, the first copies) is paid once, not per item (61 tokens, 6 of 64 experts of 3584 x 1408:
+// 58 us with an item a CTA, 52 this way).  Where the items are fewer than the SMs, a cluster of S CTAs
+// shares each item's reduction instead and adds its FP32 sums in rank order through distributed shared
+// memory.
 // The host knows only how many units there can be; each CTA sums up the experts' units from the
 // counts when it starts.
 // Rows of a segment start anywhere: the copy of X has the rows of the next expert behind the

@@ -25,8 +25,8 @@
 // What bounds it: the epilogue, which TMEM's two buffers keep in step with the MMAs.  Forward, 65536 rows
 // of 64 experts: 0.40 us a K-block (0.35 without the promotion, 0.38 with it and no TMEM loads) and 1.8 us
 // a tile; 580 us at 2816 x 4096, 2600 TFLOP/s.  WGrad: 0.56 us a K-block and 1.2 us for the tile's store,
-// 840 us; without the promotion (a multiply and an FMA an element) 590.  The epilogue's registers are full:
-// whatever adds a few to its K loop spills and costs more than it gives.
+// 840 us; without the promotion (a multiply and an FMA an element) 590.  The epilogue's registers are full (56
+// bytes are spilled in the forward, 28 in WGrad): whatever adds a few more to its K loop costs more than it gives.
 // Every mbarrier wait is bounded (FP8RL_ERR_DEVICE_TIMEOUT).
 #include "common.cuh"
 #include "experts.h"
@@ -302,9 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(x_threads(XSmem<WGRA
             }
         } else if (warp == 3) {
             // ------------------------------------------------------------ scales
-            // a warp of their own, so that they run ahead of the operands by the whole scale ring
-            // (16 K-blocks): B's come one by one from rows far apart, and with the operands' lead
-            // of 5 K-blocks the epilogue waited for them
+            // a warp of their own, so that they run ahead by the whole scale ring (16 K-blocks, WGrad 8) and
+            // not by the operands' 4 stages (B's block scales in forward and DGrad: the epilogue reads them)
             const uint64_t pol = l2_policy_evict_last();
             const int sgrp = WGRAD ? 1 : (p.nkb < S::SG ? p.nkb : S::SG);
             uint32_t it = 0, nt = 0;
