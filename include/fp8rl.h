@@ -572,7 +572,8 @@ FP8RL_API fp8rl_status fp8rl_route_topk_bwd(const fp8rl_route_bwd_args* args, in
  * count[e], in the order of p; start[0] = 0 and start[e + 1] is the next multiple of `align` after
  * them.  Every buffer of rows has R = fp8rl_expert_rows_capacity(T, k, E, align) rows, the most
  * that the layout can need; rows that hold no pair are padding behind an expert or unused at the
- * end.
+ * end.  pos and src describe the same order, as fp8rl_expert_rows leaves them (a row whose pair is
+ * not at that row in pos is not written by the gather).
  *   align = 128: training and prefill (the 128x1 groups and the GEMM tiles of an expert are its own);
  *   align = 1:   rollout, a few rows an expert (forward only; R = T k). */
 typedef struct {
